@@ -157,7 +157,7 @@ def run_reference(args, rank):
     wg, bias, off = f64(inp["w_gate"]), f64(inp["bias"]), f64(inp["logit_offset"])
     shared = (f64(inp["ws1"]), f64(inp["ws3"]), f64(inp["ws2"])) if w.n_shared else None
     ffn = (O.swiglu_ffn_fp8 if w.fp8 else O.swiglu_ffn_mxfp8 if w.mxfp8 else
-           O.swiglu_ffn_nvfp4 if w.nvfp4 else None)
+           O.swiglu_ffn_mxfp4 if w.mxfp4 else O.swiglu_ffn_nvfp4 if w.nvfp4 else None)
 
     def experts(e):
         return f64(inp["w1"][e]), f64(inp["w3"][e]), f64(inp["w2"][e])
@@ -199,6 +199,7 @@ def workload_config(w, world: int = 1) -> dict:
             "capacity": w.capacity, "parallelism": f"replicas x{world}",
             "experts_precision": ("E4M3, 1x128 / 128x128 block scales" if w.fp8 else
                                   "MXFP8: E4M3, E8M0 scale per 32 along K" if w.mxfp8 else
+                                  "MXFP4 weights (E2M1, E8M0 scale per 32 along K), MXFP8 rows" if w.mxfp4 else
                                   "NVFP4: E2M1, E4M3 scale per 16 along K, fp32 per expert matrix"
                                   if w.nvfp4 else "fp32" if w.dtype == "fp32" else "bf16")}
 
@@ -217,7 +218,7 @@ def cpu_baseline(inp, w, seconds_target=20.0, chunk=4, max_tokens=64, threads=No
     wg, bias, off = f64(inp["w_gate"]), f64(inp["bias"]), f64(inp["logit_offset"])
     shared = (f64(inp["ws1"]), f64(inp["ws3"]), f64(inp["ws2"])) if w.n_shared else None
     ffn = (O.swiglu_ffn_fp8 if w.fp8 else O.swiglu_ffn_mxfp8 if w.mxfp8 else
-           O.swiglu_ffn_nvfp4 if w.nvfp4 else None)
+           O.swiglu_ffn_mxfp4 if w.mxfp4 else O.swiglu_ffn_nvfp4 if w.nvfp4 else None)
 
     def experts(e):
         return f64(inp["w1"][e]), f64(inp["w3"][e]), f64(inp["w2"][e])
@@ -515,7 +516,7 @@ def main():
     if lay.gather_rows:        # no row gather: index maps only (the grouped FFN reads x itself)
         bytes_perm = 12 * T * k
     bytes_comb = R * d * eb + 2 * T * d * eb + 8 * T * k
-    lowp = w.fp8 or w.mxfp8 or w.nvfp4
+    lowp = w.fp8 or w.mxfp8 or w.nvfp4 or w.mxfp4
     if lowp:                   # bf16 x read once; codes + scales written per row (+ token order)
         per_elem = 0.5 + 1 / 16 if w.nvfp4 else 1 + (4 / 128 if w.fp8 else 1 / 32)
         bytes_perm = T * d * eb + (R + (T if lay.fs else 0)) * d * per_elem + 12 * T * k
@@ -599,6 +600,8 @@ def main():
             "steps": args.steps, "warmup": args.warmup, "ms_per_step": ms, "higher_is_better": True,
             "scaling": "weak", "vs_baseline": None, "dtype": ("nvfp4-e2m1 experts, fp32 router" if w.nvfp4 else
                                                               "mxfp8-e4m3 experts, fp32 router" if w.mxfp8 else
+                                                              "mxfp4-e2m1 weights, mxfp8 rows, fp32 router"
+                                                              if w.mxfp4 else
                                                               "fp8-e4m3 experts, fp32 router" if w.fp8 else
                                                               "fp32" if w.dtype == "fp32" else "bf16"),
             "data": "synthetic",
@@ -606,7 +609,7 @@ def main():
                            expert_rows=("read from x by the first grouped GEMM (cp.async)" if lay.gather_rows
                                         else "expert-ordered copy of x written by the permutation"),
                            l2=(f"inputs larger than L2 (x {T * d * eb / 1e6:.0f} MB, expert weights "
-                               f"{3 * N * d * f * (0.5 if w.nvfp4 else 1 if lowp else eb) / 1e9:.1f} GB); "
+                               f"{3 * N * d * f * (0.5 if w.nvfp4 or w.mxfp4 else 1 if lowp else eb) / 1e9:.1f} GB); "
                                "no flush")),
             "tflops": (flops_routed + flops_shared + flops_router) / (ms * 1e-3) / 1e12,
             "roofline": {"kernel": ("grouped SwiGLU FFN, routed gate/up pass + routed and shared down pass"

@@ -437,6 +437,56 @@ int moe_grouped_ffn_mxfp8(const moe_config_t* cfg, const uint8_t* xq_rows, const
                           void* y_rows, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * MXFP4 expert weights (OCP Microscaling FP4).
+ *
+ * No page defines this form: it is the 4-bit member of the OCP Microscaling formats
+ * (v1.0), beside MXFP8 above.  Format: E2M1 codes (magnitudes 0, 0.5, 1, 1.5, 2, 3, 4,
+ * 6); every 32 consecutive elements along a row share one E8M0 scale byte b, value
+ * 2^(b - 127), with b = floor(log2 amax) - 2 + 127, at least 0 (0 for an all-zero
+ * block); code = E2M1(x / 2^(b - 127)), round to nearest even, saturating at 6.  A
+ * block that holds an infinity or a NaN takes b = 255 (the format's NaN) and zero
+ * codes, and reads back as NaN.  Codes are packed two per byte, element 2i in the low
+ * nibble: [rows, cols] takes rows * cols / 2 bytes.  Scales are stored in MXFP8's tile
+ * atoms (layout and sizes above).
+ * ------------------------------------------------------------------------- */
+
+/* moe_quantize_mxfp4 -- quantise a matrix along its rows.
+ *   x        [rows, cols] of x_dtype (MOE_DTYPE_*; device), cols % 128 == 0
+ *   q        [rows, cols / 2] uint8 out; sf E8M0 scales out, plain-matrix tile atoms
+ * Expert weights [G, f, d] are quantised as rows = G * f (blocks never span rows).
+ * Errors: MOE_ERR_INVALID_ARG for a bad shape or type or a NULL or misaligned
+ * (16-byte) pointer; MOE_ERR_UNSUPPORTED past 2^43 elements.  rows = 0 is a no-op. */
+int moe_quantize_mxfp4(const void* x, int32_t x_dtype, int64_t rows, int32_t cols, uint8_t* q, uint8_t* sf,
+                       void* stream);
+
+/* moe_dequantize_mxfp4 -- y = the values that codes and scales stand for (exact in fp32
+ * and, for scales of 2^-126 and above, in bf16).
+ *   q, sf    as moe_quantize_mxfp4 writes them
+ *   y        [rows, cols] of y_dtype (MOE_DTYPE_*) out
+ * Errors: as moe_quantize_mxfp4. */
+int moe_dequantize_mxfp4(const uint8_t* q, const uint8_t* sf, int64_t rows, int32_t cols, int32_t y_dtype, void* y,
+                         void* stream);
+
+/* moe_grouped_ffn_mxfp4 -- moe_grouped_ffn_mxfp8 with MXFP4 weights: MXFP8 rows (from
+ * moe_permute_mxfp8, or moe_quantize_mxfp8 for one dense group) times MXFP4 matrices.
+ *   xq_rows, xsf_rows  [rows_cap, d] E4M3 codes; scales as tile atoms grouped by offsets
+ *   offsets            [G+1] int32 (device), as for moe_grouped_ffn
+ *   w1q/w1sf, w3q/w3sf [G f, d / 2] codes; scales as plain-matrix tile atoms
+ *   w2q/w2sf           [G d, f / 2] codes; scales as plain-matrix tile atoms
+ *   hq/hsf_scratch     [rows_cap, f] E4M3 codes; scales as tile atoms grouped by offsets
+ *   y_rows             [rows_cap, d] bf16 out (rows >= offsets[G] untouched)
+ * One fp32 TMEM accumulator over the whole K range (block-scaled tcgen05 MMA, E4M3 x
+ * E2M1); h = silu(W1 x) * (W3 x) in fp32, re-quantised to MXFP8 along f.
+ * Errors: MOE_ERR_UNSUPPORTED unless a bf16 config with d % 128 == f % 128 == 0;
+ * MOE_ERR_INVALID_ARG for G outside [1, 512], NULL or misaligned buffers (16-byte;
+ * the weights' codes 32-byte). */
+int moe_grouped_ffn_mxfp4(const moe_config_t* cfg, const uint8_t* xq_rows, const uint8_t* xsf_rows,
+                          int64_t rows_cap, const int32_t* offsets, int32_t G, const uint8_t* w1q,
+                          const uint8_t* w1sf, const uint8_t* w3q, const uint8_t* w3sf, const uint8_t* w2q,
+                          const uint8_t* w2sf, int32_t f, uint8_t* hq_scratch, uint8_t* hsf_scratch,
+                          void* y_rows, void* stream);
+
+/* ---------------------------------------------------------------------------
  * NVFP4 expert compute.
  *
  * Defines: the MoE common-taste page, section 2 (its table names NVFP4 beside FP8 /

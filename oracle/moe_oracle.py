@@ -777,6 +777,49 @@ def swiglu_ffn_nvfp4(x_rows, w1, w3, w2, hidden_out: bool = False):
 
 
 # ---------------------------------------------------------------------------
+# MXFP4 (OCP Microscaling) expert weights under MXFP8 rows
+# ---------------------------------------------------------------------------
+E2M1_EMAX = 2          # exponent of E2M1's largest normal (6 = 1.5 * 2^2)
+
+
+def quantize_mxfp4(x: np.ndarray, block: int = MX_BLOCK) -> tuple:
+    """MXFP4 quantisation along each row: quantize_mxfp8's scheme with E2M1 elements, so
+    e = floor(log2(amax)) - 2 clamped at -127 (an all-zero block takes -127) and
+    elements E2M1(x / 2^e), saturating at 6.  A block with an infinity or a NaN takes
+    e = 128 (scale byte 255, the format's NaN) and zero elements.
+    Returns (codes as float64 values, exponents e [rows, cols/block] int).
+    """
+    x = np.asarray(x, np.float64)
+    R, C = x.shape
+    blocks = x.reshape(R, C // block, block)
+    finite = np.isfinite(blocks).all(axis=2)
+    blocks = np.where(finite[:, :, None], blocks, 0.0)
+    amax = np.max(np.abs(blocks), axis=2)
+    _, ex = np.frexp(amax)                         # amax = m 2^ex, m in [0.5, 1)
+    e = np.where(amax > 0, ex.astype(np.int64) - 1 - E2M1_EMAX, -127)
+    e = np.maximum(e, -127)
+    q = round_e2m1(blocks / (2.0 ** e)[:, :, None]).reshape(R, C)
+    return q, np.where(finite, e, 128)
+
+
+def dequantize_mxfp4(q: np.ndarray, e: np.ndarray, block: int = MX_BLOCK) -> np.ndarray:
+    e = np.asarray(e, np.float64)
+    s = np.where(e == 128, np.nan, 2.0 ** np.where(e == 128, 0, e))
+    return np.asarray(q, np.float64) * np.repeat(s, block, axis=1)
+
+
+def swiglu_ffn_mxfp4(x_rows, w1, w3, w2, hidden_out: bool = False):
+    """The SwiGLU expert with MXFP4 weights: x (along d) and h (along d_ff) in MXFP8, the
+    matrices in MXFP4 along the contraction dimension; fp64 products of the dequantised
+    values."""
+    xd = dequantize_mxfp8(*quantize_mxfp8(x_rows))
+    w1d, w3d, w2d = (dequantize_mxfp4(*quantize_mxfp4(w)) for w in (w1, w3, w2))
+    h = silu(xd @ w1d.T) * (xd @ w3d.T)
+    y = dequantize_mxfp8(*quantize_mxfp8(h)) @ w2d.T
+    return (y, h) if hidden_out else y
+
+
+# ---------------------------------------------------------------------------
 # Expert parallelism: the exchange plan
 # ---------------------------------------------------------------------------
 def ep_plan(offsets_all: np.ndarray, rank: int) -> dict:

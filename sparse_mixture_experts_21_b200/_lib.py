@@ -29,6 +29,7 @@ EXPORTED = ("moe_capacity", "moe_route_partials", "moe_workspace_size", "moe_rou
             "moe_device_status", "moe_status_string", "moe_permute_noalloc", "moe_bias_update_ema",
             "moe_bias_update_seq", "moe_route_scores", "moe_expert_choice", "moe_combine_ec",
             "moe_selftest_wait_timeout", "moe_quantize_fp8", "moe_permute_fp8", "moe_grouped_ffn_fp8",
+            "moe_quantize_mxfp4", "moe_dequantize_mxfp4", "moe_grouped_ffn_mxfp4",
             "moe_quantize_mxfp8", "moe_permute_mxfp8", "moe_grouped_ffn_mxfp8", "moe_quantize_nvfp4",
             "moe_permute_nvfp4", "moe_grouped_ffn_nvfp4", "moe_ep_plan",
             "moe_rows_move", "moe_peer_export", "moe_peer_import", "moe_peer_close", "moe_ep_peer_plan",
@@ -132,6 +133,10 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         "moe_combine_peer": [cfgp, vp, vp, vp, vp, vp, vp, vp],
         "moe_permute_mxfp8": [cfgp, vp, vp, vp, vp, vp, vp, vp, vp, vp],
         "moe_grouped_ffn_mxfp8": [cfgp, vp, vp, c_int64, vp, c_int32, vp, vp, vp, vp, vp, vp, c_int32, vp, vp,
+                                  vp, vp],
+        "moe_quantize_mxfp4": [vp, c_int32, c_int64, c_int32, vp, vp, vp],
+        "moe_dequantize_mxfp4": [vp, vp, c_int64, c_int32, c_int32, vp, vp],
+        "moe_grouped_ffn_mxfp4": [cfgp, vp, vp, c_int64, vp, c_int32, vp, vp, vp, vp, vp, vp, c_int32, vp, vp,
                                   vp, vp],
         "moe_quantize_nvfp4": [vp, c_int64, c_int32, c_int32, vp, vp, vp, vp],
         "moe_permute_nvfp4": [cfgp, vp, vp, vp, vp, vp, vp, vp, vp, vp],
@@ -315,6 +320,59 @@ def moe_grouped_ffn_mxfp8(cfg, xq_rows, xsf_rows, rows_cap, offsets, G, w1q, w1s
         ctypes.byref(cfg), _ptr(xq_rows), _ptr(xsf_rows), int(rows_cap), _ptr(offsets), int(G), _ptr(w1q),
         _ptr(w1sf), _ptr(w3q), _ptr(w3sf), _ptr(w2q), _ptr(w2sf), int(f), _ptr(hq_scratch), _ptr(hsf_scratch),
         _ptr(y_rows), _stream(stream)))
+
+
+def _expect(name: str, t: torch.Tensor, dtype: torch.dtype, numel: int, device=None) -> None:
+    """Refuse a buffer of another type or device, or one too small for what is written or read."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.numel() < numel:
+        raise ValueError(f"{name} holds {t.numel()} elements of the {numel} it needs")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _float_type(name: str, t: torch.Tensor) -> int:
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"{name} must be float32 or bfloat16, not {t.dtype}")
+    return DTYPE_F32 if t.dtype == torch.float32 else DTYPE_BF16
+
+
+def moe_quantize_mxfp4(x, q, sf, stream=None):
+    """MXFP4-quantise an fp32 or bf16 matrix [rows, cols] along its rows: packed E2M1 codes
+    (q: rows x cols / 2 bytes) and E8M0 scales (sf from mx_scales(rows, cols)).  Runs on x's
+    device."""
+    rows, cols = x.shape
+    dt = _float_type("x", x)
+    if cols % 128 == 0:
+        _expect("q", q, torch.uint8, rows * cols // 2, x.device)
+        _expect("sf", sf, torch.uint8, (rows + 127) // 128 * cols * 4, x.device)
+    with torch.cuda.device(x.device):
+        _check("moe_quantize_mxfp4", load().moe_quantize_mxfp4(
+            _ptr(x), dt, int(rows), int(cols), _ptr(q), _ptr(sf), _stream(stream)))
+
+
+def moe_dequantize_mxfp4(q, sf, y, stream=None):
+    """y [rows, cols] (fp32 or bf16) = the values that codes q and scales sf stand for.  Runs on
+    y's device."""
+    rows, cols = y.shape
+    dt = _float_type("y", y)
+    if cols % 128 == 0:
+        _expect("q", q, torch.uint8, rows * cols // 2, y.device)
+        _expect("sf", sf, torch.uint8, (rows + 127) // 128 * cols * 4, y.device)
+    with torch.cuda.device(y.device):
+        _check("moe_dequantize_mxfp4", load().moe_dequantize_mxfp4(
+            _ptr(q), _ptr(sf), int(rows), int(cols), dt, _ptr(y), _stream(stream)))
+
+
+def moe_grouped_ffn_mxfp4(cfg, xq_rows, xsf_rows, rows_cap, offsets, G, w1q, w1sf, w3q, w3sf, w2q, w2sf, f,
+                          hq_scratch, hsf_scratch, y_rows, stream=None):
+    """moe_grouped_ffn_mxfp8 with MXFP4 weights (packed codes from moe_quantize_mxfp4)."""
+    with torch.cuda.device(y_rows.device):
+        _check("moe_grouped_ffn_mxfp4", load().moe_grouped_ffn_mxfp4(
+            ctypes.byref(cfg), _ptr(xq_rows), _ptr(xsf_rows), int(rows_cap), _ptr(offsets), int(G), _ptr(w1q),
+            _ptr(w1sf), _ptr(w3q), _ptr(w3sf), _ptr(w2q), _ptr(w2sf), int(f), _ptr(hq_scratch), _ptr(hsf_scratch),
+            _ptr(y_rows), _stream(stream)))
 
 
 def nv_scales(rows: int, cols: int, device, groups: int = 0) -> torch.Tensor:

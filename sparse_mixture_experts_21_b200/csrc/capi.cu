@@ -46,6 +46,8 @@ namespace capi {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+
 int check_config(const moe_config_t* c) {
   if (!c) return MOE_ERR_INVALID_ARG;
   if (c->T < 0 || c->d_model <= 0 || (c->d_model % 8) != 0) return MOE_ERR_INVALID_ARG;
@@ -402,6 +404,55 @@ int moe_grouped_ffn_mxfp8(const moe_config_t* cfg, const uint8_t* xq_rows, const
   return from_cuda(launch_ffn_mx(xq_rows, xsf_rows, rows_cap, offsets, G, w1q, w1sf, w3q, w3sf, w2q, w2sf,
                                  cfg->d_model, f, hq_scratch, hsf_scratch, y_rows,
                                  static_cast<cudaStream_t>(stream)));
+}
+
+int moe_quantize_mxfp4(const void* x, int32_t x_dtype, int64_t rows, int32_t cols, uint8_t* q, uint8_t* sf,
+                       void* stream) {
+  if (rows < 0 || cols <= 0 || (cols % 128) != 0) return MOE_ERR_INVALID_ARG;
+  if (x_dtype != MOE_DTYPE_F32 && x_dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (rows > ((int64_t)1 << 43) / cols) return MOE_ERR_UNSUPPORTED;
+  if (!x || !q || !sf || !aligned16(x) || !aligned16(q) || !aligned16(sf)) return MOE_ERR_INVALID_ARG;
+  return from_cuda(launch_mx4_quant(x, x_dtype == MOE_DTYPE_F32, rows, cols, q, sf, static_cast<cudaStream_t>(stream)));
+}
+
+int moe_dequantize_mxfp4(const uint8_t* q, const uint8_t* sf, int64_t rows, int32_t cols, int32_t y_dtype, void* y,
+                         void* stream) {
+  if (rows < 0 || cols <= 0 || (cols % 128) != 0) return MOE_ERR_INVALID_ARG;
+  if (y_dtype != MOE_DTYPE_F32 && y_dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (rows > ((int64_t)1 << 43) / cols) return MOE_ERR_UNSUPPORTED;
+  if (!q || !sf || !y || !aligned16(q) || !aligned16(sf) || !aligned16(y)) return MOE_ERR_INVALID_ARG;
+  return from_cuda(launch_mx4_dequant(q, sf, rows, cols, y_dtype == MOE_DTYPE_F32, y, static_cast<cudaStream_t>(stream)));
+}
+
+int moe_grouped_ffn_mxfp4(const moe_config_t* cfg, const uint8_t* xq_rows, const uint8_t* xsf_rows,
+                          int64_t rows_cap, const int32_t* offsets, int32_t G, const uint8_t* w1q,
+                          const uint8_t* w1sf, const uint8_t* w3q, const uint8_t* w3sf, const uint8_t* w2q,
+                          const uint8_t* w2sf, int32_t f, uint8_t* hq_scratch, uint8_t* hsf_scratch,
+                          void* y_rows, void* stream) {
+  const int st = check_config(cfg);
+  if (st != MOE_OK) return st;
+  if (rows_cap < 0 || G < 1 || G > 512 || f <= 0) return MOE_ERR_INVALID_ARG;
+  if (cfg->x_dtype != MOE_DTYPE_BF16 || (cfg->d_model % 128) != 0 || (f % 128) != 0)
+    return MOE_ERR_UNSUPPORTED;
+  if (!offsets) return MOE_ERR_INVALID_ARG;
+  if (rows_cap == 0) return MOE_OK;
+  if (rows_cap > (int64_t)INT32_MAX || (int64_t)G * cfg->d_model > (int64_t)INT32_MAX ||
+      (int64_t)G * f > (int64_t)INT32_MAX)
+    return MOE_ERR_UNSUPPORTED;
+  if (!xq_rows || !xsf_rows || !w1q || !w1sf || !w3q || !w3sf || !w2q || !w2sf || !hq_scratch ||
+      !hsf_scratch || !y_rows)
+    return MOE_ERR_INVALID_ARG;
+  // the weights' tensor maps of 4-bit codes want 32-byte bases
+  if (!aligned16(xq_rows) || !aligned32(w1q) || !aligned32(w3q) || !aligned32(w2q) || !aligned16(hq_scratch) ||
+      !aligned16(y_rows))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(xsf_rows) || !aligned16(w1sf) || !aligned16(w3sf) || !aligned16(w2sf) || !aligned16(hsf_scratch))
+    return MOE_ERR_INVALID_ARG;
+  return from_cuda(launch_ffn_mx4(xq_rows, xsf_rows, rows_cap, offsets, G, w1q, w1sf, w3q, w3sf, w2q, w2sf,
+                                  cfg->d_model, f, hq_scratch, hsf_scratch, y_rows,
+                                  static_cast<cudaStream_t>(stream)));
 }
 
 int moe_quantize_nvfp4(const void* x, int64_t rows, int32_t cols, int32_t tensor_rows, uint8_t* q, uint8_t* sf,

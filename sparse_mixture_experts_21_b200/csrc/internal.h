@@ -14,6 +14,7 @@ namespace moe {
 // box_rows rows, 128-byte swizzle, zero fill out of bounds.
 bool make_map_bf16(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows);
 bool make_map_u8(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows);
+bool make_map_u4(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows);
 bool make_map_bf16_store32(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols);
 
 // Padded expert count, tokens per block and scratch of the fused router.
@@ -109,6 +110,14 @@ cudaError_t launch_ffn_mx(const uint8_t* xq, const uint8_t* xsf, int64_t rows_ca
                           const uint8_t* w1q, const uint8_t* w1sf, const uint8_t* w3q, const uint8_t* w3sf,
                           const uint8_t* w2q, const uint8_t* w2sf, int d, int f, uint8_t* hq, uint8_t* hsf,
                           void* y, cudaStream_t s);
+cudaError_t launch_mx4_quant(const void* x, bool f32, int64_t rows, int cols, uint8_t* q, uint8_t* sf,
+                             cudaStream_t s);
+cudaError_t launch_mx4_dequant(const uint8_t* q, const uint8_t* sf, int64_t rows, int cols, bool f32, void* y,
+                               cudaStream_t s);
+cudaError_t launch_ffn_mx4(const uint8_t* xq, const uint8_t* xsf, int64_t rows_cap, const int32_t* offsets, int G,
+                           const uint8_t* w1q, const uint8_t* w1sf, const uint8_t* w3q, const uint8_t* w3sf,
+                           const uint8_t* w2q, const uint8_t* w2sf, int d, int f, uint8_t* hq, uint8_t* hsf,
+                           void* y, cudaStream_t s);
 cudaError_t launch_nv_quant_rows(const void* x, int64_t rows, int cols, int tensor_rows, uint8_t* q, uint8_t* sf,
                                  float* g, cudaStream_t s);
 cudaError_t launch_nv_quant_scatter(const void* x, int64_t T, int k, int d, int N, const int32_t* topk_idx,

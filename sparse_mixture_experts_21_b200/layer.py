@@ -42,7 +42,7 @@ class MoELayer:
         whole group's batch (each rank's sufficient statistics summed over the
         group) and the bias update uses the counts summed over the group, so all
         replicas keep the same selection bias."""
-        lowp = w.fp8 or w.mxfp8 or w.nvfp4
+        lowp = w.fp8 or w.mxfp8 or w.nvfp4 or w.mxfp4
         if w.expert_choice and lowp:
             raise ValueError("expert-choice routing runs bf16 or fp32 experts")
         if lowp and (w.dtype != "bf16" or w.d % 128 or w.f % 128 or w.f_shared % 128):
@@ -151,12 +151,14 @@ class MoELayer:
     def _init_fp8(self, z):
         """Low-precision experts: quantise the weights once (fine-grained FP8: 128 x 128
         blocks with fp32 scales; MXFP8: 1 x 32 blocks along K with E8M0 scales; NVFP4:
-        1 x 16 blocks along K with E4M3 scales and one fp32 scale per expert matrix) and
+        1 x 16 blocks along K with E4M3 scales and one fp32 scale per expert matrix; MXFP4:
+        1 x 32 blocks of 4-bit codes with E8M0 scales, under MXFP8 rows) and
         hold code buffers for the permuted rows, the hidden rows and the shared experts'
         input in place of the bf16 ones."""
         w, W, T, d, N, k = self.w, self.weights, self.w.T, self.w.d, self.w.N, self.w.k
         u8 = torch.uint8
-        mx, nv = w.mxfp8, w.nvfp4
+        mx4, nv = w.mxfp4, w.nvfp4
+        mx = w.mxfp8 or mx4                    # rows (x and h) in MXFP8
         # scales of grouped (permuted) rows: tile atoms need one spare tile per group
         if nv:
             sfa = lambda rows, cols, groups=0: L.nv_scales(rows, cols, self.dev, groups)  # noqa: E731
@@ -168,7 +170,11 @@ class MoELayer:
 
         def quant_w(t):
             m = t.reshape(-1, t.shape[-1])
-            q = z(m.shape[0], cw(m.shape[1]), dtype=u8)
+            q = z(m.shape[0], m.shape[1] // 2 if mx4 else cw(m.shape[1]), dtype=u8)
+            if mx4:
+                sc = L.mx_scales(m.shape[0], m.shape[1], self.dev)
+                L.moe_quantize_mxfp4(m, q, sc)
+                return q, sc
             if nv:
                 # one tensor scale per expert matrix (t is [experts, rows, cols] or one matrix)
                 per = t.shape[-2]
@@ -199,7 +205,8 @@ class MoELayer:
         if self.w.nvfp4:
             L.moe_grouped_ffn_nvfp4(c, xq, xs, rows, offsets, G, *w1, *w3, *w2, f, hq, hsc, y, s)
             return
-        fn = L.moe_grouped_ffn_mxfp8 if self.w.mxfp8 else L.moe_grouped_ffn_fp8
+        fn = (L.moe_grouped_ffn_mxfp4 if self.w.mxfp4 else
+              L.moe_grouped_ffn_mxfp8 if self.w.mxfp8 else L.moe_grouped_ffn_fp8)
         fn(c, xq, xs, rows, offsets, G, *w1, *w3, *w2, f, hq, hsc, y, s)
 
     # the launches of one layer forward; `x` is [T, d] on the device.  `marks`, if
@@ -212,7 +219,7 @@ class MoELayer:
         rec = (lambda i: marks[i].record(s)) if marks is not None else (lambda i: None)
         if self.w.expert_choice:
             return self._forward_ec(x, s, rec, y)
-        lowp = self.w.fp8 or self.w.mxfp8 or self.w.nvfp4
+        lowp = self.w.fp8 or self.w.mxfp8 or self.w.nvfp4 or self.w.mxfp4
         rec(0)
         join = None
         side_work = self.overlap_shared or self.split_shared
@@ -229,7 +236,7 @@ class MoELayer:
                 if lowp:
                     if self.w.nvfp4:
                         L.moe_quantize_nvfp4(x, self.xq, self.xs, stream=side)
-                    elif self.w.mxfp8:
+                    elif self.w.mxfp8 or self.w.mxfp4:
                         L.moe_quantize_mxfp8(x, self.xq, self.xs, side)
                     else:
                         L.moe_quantize_fp8(x, 1, self.xq, self.xs, side)
@@ -251,7 +258,7 @@ class MoELayer:
         if self.w.nvfp4:
             L.moe_permute_nvfp4(c, x, self.topk_idx, self.row_of_slot, self.offsets, self.xq_perm, self.xs_perm,
                                 self.xq if tok else None, self.xs if tok else None, s)
-        elif self.w.mxfp8:
+        elif self.w.mxfp8 or self.w.mxfp4:
             L.moe_permute_mxfp8(c, x, self.topk_idx, self.row_of_slot, self.offsets, self.xq_perm, self.xs_perm,
                                 self.xq if tok else None, self.xs if tok else None, s)
         elif fp8:
