@@ -689,6 +689,55 @@ int moe_combine(const moe_config_t* cfg, const void* y_perm, const int32_t* row_
                 void* stream);
 
 /* ---------------------------------------------------------------------------
+ * moe_few_tokens -- the whole layer for 1 to 64 tokens in one launch.
+ *
+ * Defines: the layer of the calls above (route, capacity drop, experts, shared expert,
+ * weighted sum), as a step of token-by-token serving needs it: with few tokens the
+ * layer is bound by the bytes of the picked experts' weights, and every weight is read
+ * once.  Selection, ties, capacity and weights are moe_route's and moe_permute's
+ * (logits in fp32); for each token
+ *   y = shared_weight * shared(x) + sum over its kept picks of w * E(x),
+ * E(x) = W2 (silu(W1 x) * (W3 x)), the hidden row rounded to x's type, every sum in
+ * fp32, experts in ascending order.  No statistics are written and no bias is updated.
+ *   cfg         T <= 64 (0: no-op); x_dtype and all other options as for moe_route
+ *   x           [T, d] x_dtype
+ *   w_gate      [N, d] fp32 (N + 1 rows with cfg->shared_sink)
+ *   logit_offset, bias  [N] fp32 or NULL, as for moe_route
+ *   w1, w3      [N, f, d]; w2 [N, d, f] x_dtype (f = cfg->d_ff, a multiple of 8)
+ *   ws1, ws3    [f_shared, d]; ws2 [d, f_shared] x_dtype: the shared experts concatenated
+ *               along the hidden dimension; ignored with f_shared = 0
+ *   f_shared    total hidden width of the shared experts, a multiple of 8, or 0
+ *   topk_idx    [T, k] int32 out, topk_w [T, k] fp32 out: as moe_route writes them
+ *   y           [T, d] x_dtype out (must not overlap x)
+ *   ws          scratch of at least moe_few_tokens_workspace_size() bytes (contents on
+ *               entry ignored; clobbered).  It holds the counters that the launch's
+ *               blocks wait on: calls that may overlap on the GPU (two streams, two
+ *               replayed graphs) need a workspace each.
+ * The launch is cooperative, one block on every SM; it starts when all of them are free.
+ * Errors: MOE_ERR_UNSUPPORTED for T > 64; MOE_ERR_INVALID_ARG for a bad config, a bad
+ * f_shared, or a NULL or misaligned (16-byte; 4-byte for [N] and [T, k] arrays) buffer;
+ * MOE_ERR_WORKSPACE_TOO_SMALL.
+ * ------------------------------------------------------------------------- */
+int moe_few_tokens_workspace_size(const moe_config_t* cfg, int32_t f_shared, size_t* bytes);
+int moe_few_tokens(const moe_config_t* cfg, const void* x, const float* w_gate, const float* logit_offset,
+                   const float* bias, const void* w1, const void* w3, const void* w2, const void* ws1,
+                   const void* ws3, const void* ws2, int32_t f_shared, int32_t* topk_idx, float* topk_w, void* y,
+                   void* ws, size_t ws_bytes, void* stream);
+
+/* moe_few_tokens_mxfp4 -- moe_few_tokens with MXFP4 expert weights (routed and shared),
+ * as moe_quantize_mxfp4 writes them (rows = N * f or N * d).  x and the hidden rows stay
+ * bf16: with few tokens their bytes do not count, so they are not quantised as
+ * moe_grouped_ffn_mxfp4's rows are.
+ * Errors: as moe_few_tokens; MOE_ERR_UNSUPPORTED unless a bf16 config with d, f and
+ * f_shared multiples of 128. */
+int moe_few_tokens_mxfp4(const moe_config_t* cfg, const void* x, const float* w_gate, const float* logit_offset,
+                         const float* bias, const uint8_t* w1q, const uint8_t* w1sf, const uint8_t* w3q,
+                         const uint8_t* w3sf, const uint8_t* w2q, const uint8_t* w2sf, const uint8_t* ws1q,
+                         const uint8_t* ws1sf, const uint8_t* ws3q, const uint8_t* ws3sf, const uint8_t* ws2q,
+                         const uint8_t* ws2sf, int32_t f_shared, int32_t* topk_idx, float* topk_w, void* y,
+                         void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
  * moe_router_stats -- router statistics in fixed reduction order.
  *
  * Defines: llm-compass "负载均衡" (L_aux = alpha N sum f_i P_i), the Practice page's

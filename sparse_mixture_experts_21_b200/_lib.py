@@ -30,6 +30,7 @@ EXPORTED = ("moe_capacity", "moe_route_partials", "moe_workspace_size", "moe_rou
             "moe_bias_update_seq", "moe_route_scores", "moe_expert_choice", "moe_combine_ec",
             "moe_selftest_wait_timeout", "moe_quantize_fp8", "moe_permute_fp8", "moe_grouped_ffn_fp8",
             "moe_quantize_mxfp4", "moe_dequantize_mxfp4", "moe_grouped_ffn_mxfp4",
+            "moe_few_tokens_workspace_size", "moe_few_tokens", "moe_few_tokens_mxfp4",
             "moe_quantize_mxfp8", "moe_permute_mxfp8", "moe_grouped_ffn_mxfp8", "moe_quantize_nvfp4",
             "moe_permute_nvfp4", "moe_grouped_ffn_nvfp4", "moe_ep_plan",
             "moe_rows_move", "moe_peer_export", "moe_peer_import", "moe_peer_close", "moe_ep_peer_plan",
@@ -138,6 +139,9 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         "moe_dequantize_mxfp4": [vp, vp, c_int64, c_int32, c_int32, vp, vp],
         "moe_grouped_ffn_mxfp4": [cfgp, vp, vp, c_int64, vp, c_int32, vp, vp, vp, vp, vp, vp, c_int32, vp, vp,
                                   vp, vp],
+        "moe_few_tokens_workspace_size": [cfgp, c_int32, POINTER(c_size_t)],
+        "moe_few_tokens": [cfgp] + [vp] * 10 + [c_int32, vp, vp, vp, vp, c_size_t, vp],
+        "moe_few_tokens_mxfp4": [cfgp] + [vp] * 16 + [c_int32, vp, vp, vp, vp, c_size_t, vp],
         "moe_quantize_nvfp4": [vp, c_int64, c_int32, c_int32, vp, vp, vp, vp],
         "moe_permute_nvfp4": [cfgp, vp, vp, vp, vp, vp, vp, vp, vp, vp],
         "moe_grouped_ffn_nvfp4": [cfgp, vp, vp, c_int64, vp, c_int32, vp, vp, vp, vp, vp, vp, vp, vp, vp, c_int32,
@@ -473,6 +477,64 @@ def moe_combine_peer(cfg, row_addr, row_of_slot, topk_w, shared_out, y, stream=N
     _check("moe_combine_peer", load().moe_combine_peer(
         ctypes.byref(cfg), _ptr(row_addr), _ptr(row_of_slot), _ptr(topk_w), _ptr(shared_out), _ptr(shared_w),
         _ptr(y), _stream(stream)))
+
+
+FEW_TOKENS_MAX = 64
+
+
+def few_tokens_workspace_size(cfg: MoeConfig, f_shared: int = 0) -> int:
+    """Bytes of scratch for moe_few_tokens and moe_few_tokens_mxfp4."""
+    out = c_size_t()
+    _check("moe_few_tokens_workspace_size",
+           load().moe_few_tokens_workspace_size(ctypes.byref(cfg), int(f_shared), ctypes.byref(out)))
+    return out.value
+
+
+def _few_check(cfg, x, w_gate, logit_offset, bias, weights, sizes, wtype, topk_idx, topk_w, y, ws):
+    T, N, k, d, dev = cfg.T, cfg.n_experts, cfg.top_k, cfg.d_model, x.device
+    xt = torch.float32 if cfg.x_dtype == DTYPE_F32 else torch.bfloat16
+    _expect("x", x, xt, T * d)
+    _expect("y", y, xt, T * d, dev)
+    _expect("w_gate", w_gate, torch.float32, (N + cfg.shared_sink) * d, dev)
+    for name, t in (("logit_offset", logit_offset), ("bias", bias)):
+        if t is not None:
+            _expect(name, t, torch.float32, N, dev)
+    _expect("topk_idx", topk_idx, torch.int32, T * k, dev)
+    _expect("topk_w", topk_w, torch.float32, T * k, dev)
+    _expect("ws", ws, torch.uint8, 0, dev)
+    for i, (t, n) in enumerate(zip(weights, sizes)):
+        if n:
+            _expect(f"expert weight {i}", t, wtype or xt, n, dev)
+
+
+def moe_few_tokens(cfg, x, w_gate, logit_offset, bias, w1, w3, w2, ws1, ws3, ws2, f_shared, topk_idx, topk_w, y, ws,
+                   stream=None):
+    """The whole layer for 1 to 64 tokens (cfg.T) in one launch; ws: a uint8 tensor of
+    few_tokens_workspace_size(cfg, f_shared), one per call that may overlap another.  Runs on
+    x's device."""
+    n, s = cfg.n_experts * cfg.d_ff * cfg.d_model, f_shared * cfg.d_model
+    _few_check(cfg, x, w_gate, logit_offset, bias, (w1, w3, w2, ws1, ws3, ws2), (n, n, n, s, s, s), None, topk_idx,
+               topk_w, y, ws)
+    with torch.cuda.device(x.device):
+        _check("moe_few_tokens", load().moe_few_tokens(
+            ctypes.byref(cfg), _ptr(x), _ptr(w_gate), _ptr(logit_offset), _ptr(bias), _ptr(w1), _ptr(w3), _ptr(w2),
+            _ptr(ws1), _ptr(ws3), _ptr(ws2), int(f_shared), _ptr(topk_idx), _ptr(topk_w), _ptr(y), _ptr(ws),
+            ws.numel(), _stream(stream)))
+
+
+def moe_few_tokens_mxfp4(cfg, x, w_gate, logit_offset, bias, w1, w3, w2, ws1, ws3, ws2, f_shared, topk_idx, topk_w, y,
+                         ws, stream=None):
+    """moe_few_tokens with MXFP4 weights: each a pair (codes, scales) as moe_quantize_mxfp4
+    writes them, the shared ones None with f_shared = 0."""
+    n, s = cfg.n_experts * cfg.d_ff * cfg.d_model, f_shared * cfg.d_model
+    pairs = [p if p is not None else (None, None) for p in (w1, w3, w2, ws1, ws3, ws2)]
+    flat = [t for p in pairs for t in p]
+    _few_check(cfg, x, w_gate, logit_offset, bias, flat, (n // 2, n // 32) * 3 + (s // 2, s // 32) * 3, torch.uint8,
+               topk_idx, topk_w, y, ws)
+    with torch.cuda.device(x.device):
+        _check("moe_few_tokens_mxfp4", load().moe_few_tokens_mxfp4(
+            ctypes.byref(cfg), _ptr(x), _ptr(w_gate), _ptr(logit_offset), _ptr(bias), *(_ptr(t) for t in flat),
+            int(f_shared), _ptr(topk_idx), _ptr(topk_w), _ptr(y), _ptr(ws), ws.numel(), _stream(stream)))
 
 
 def moe_combine(cfg, y_perm, row_of_slot, topk_w, shared_out, y, stream=None, shared_w=None):

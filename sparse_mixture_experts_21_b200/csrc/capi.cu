@@ -100,6 +100,37 @@ int from_cuda(cudaError_t e) {
   return MOE_ERR_CUDA;
 }
 
+// The few-token layer's checks, common to its two weight forms.
+int check_few(const moe_config_t* cfg, int32_t f_shared, bool mxfp4) {
+  const int st = check_config(cfg);
+  if (st != MOE_OK) return st;
+  if (cfg->d_ff <= 0 || (cfg->d_ff % 8) != 0 || f_shared < 0 || (f_shared % 8) != 0) return MOE_ERR_INVALID_ARG;
+  if (cfg->T > 64) return MOE_ERR_UNSUPPORTED;
+  if (mxfp4 && (cfg->x_dtype != MOE_DTYPE_BF16 || (cfg->d_model % 128) != 0 || (cfg->d_ff % 128) != 0 ||
+                (f_shared % 128) != 0))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+int few_tokens(const moe_config_t* cfg, const void* x, const float* w_gate, const float* logit_offset,
+               const float* bias, bool mxfp4, const void* const* w, const uint8_t* const* sf, int32_t f_shared,
+               int32_t* topk_idx, float* topk_w, void* y, void* ws, size_t ws_bytes, void* stream) {
+  const int st = check_few(cfg, f_shared, mxfp4);
+  if (st != MOE_OK) return st;
+  if (cfg->T == 0) return MOE_OK;
+  if (!x || !w_gate || !topk_idx || !topk_w || !y) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(w_gate) || !aligned16(y)) return MOE_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(topk_idx) | reinterpret_cast<uintptr_t>(topk_w) |
+       reinterpret_cast<uintptr_t>(logit_offset) | reinterpret_cast<uintptr_t>(bias)) & 3u)
+    return MOE_ERR_INVALID_ARG;
+  for (int i = 0; i < (f_shared > 0 ? 6 : 3); ++i)
+    if (!w[i] || !aligned16(w[i]) || (mxfp4 && (!sf[i] || !aligned16(sf[i])))) return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < few_workspace_bytes(*cfg, f_shared)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (!ws || !aligned16(ws)) return MOE_ERR_INVALID_ARG;
+  return from_cuda(launch_few(*cfg, capacity_of(*cfg), x, w_gate, logit_offset, bias, mxfp4, w, sf, f_shared,
+                              topk_idx, topk_w, y, ws, static_cast<cudaStream_t>(stream)));
+}
+
 // Self-test of the bounded wait: one thread waits on an mbarrier that nothing
 // ever arrives on (its own arrival count is 2 and it arrives once), gives up after
 // `limit` cycles, records MOE_ERR_DEVICE_TIMEOUT and returns normally.
@@ -453,6 +484,35 @@ int moe_grouped_ffn_mxfp4(const moe_config_t* cfg, const uint8_t* xq_rows, const
   return from_cuda(launch_ffn_mx4(xq_rows, xsf_rows, rows_cap, offsets, G, w1q, w1sf, w3q, w3sf, w2q, w2sf,
                                   cfg->d_model, f, hq_scratch, hsf_scratch, y_rows,
                                   static_cast<cudaStream_t>(stream)));
+}
+
+int moe_few_tokens_workspace_size(const moe_config_t* cfg, int32_t f_shared, size_t* bytes) {
+  const int st = check_few(cfg, f_shared, false);
+  if (st != MOE_OK) return st;
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  *bytes = few_workspace_bytes(*cfg, f_shared);
+  return MOE_OK;
+}
+
+int moe_few_tokens(const moe_config_t* cfg, const void* x, const float* w_gate, const float* logit_offset,
+                   const float* bias, const void* w1, const void* w3, const void* w2, const void* ws1,
+                   const void* ws3, const void* ws2, int32_t f_shared, int32_t* topk_idx, float* topk_w, void* y,
+                   void* ws, size_t ws_bytes, void* stream) {
+  const void* w[6] = {w1, w3, w2, ws1, ws3, ws2};
+  return few_tokens(cfg, x, w_gate, logit_offset, bias, false, w, nullptr, f_shared, topk_idx, topk_w, y, ws,
+                    ws_bytes, stream);
+}
+
+int moe_few_tokens_mxfp4(const moe_config_t* cfg, const void* x, const float* w_gate, const float* logit_offset,
+                         const float* bias, const uint8_t* w1q, const uint8_t* w1sf, const uint8_t* w3q,
+                         const uint8_t* w3sf, const uint8_t* w2q, const uint8_t* w2sf, const uint8_t* ws1q,
+                         const uint8_t* ws1sf, const uint8_t* ws3q, const uint8_t* ws3sf, const uint8_t* ws2q,
+                         const uint8_t* ws2sf, int32_t f_shared, int32_t* topk_idx, float* topk_w, void* y,
+                         void* ws, size_t ws_bytes, void* stream) {
+  const void* w[6] = {w1q, w3q, w2q, ws1q, ws3q, ws2q};
+  const uint8_t* sf[6] = {w1sf, w3sf, w2sf, ws1sf, ws3sf, ws2sf};
+  return few_tokens(cfg, x, w_gate, logit_offset, bias, true, w, sf, f_shared, topk_idx, topk_w, y, ws, ws_bytes,
+                    stream);
 }
 
 int moe_quantize_nvfp4(const void* x, int64_t rows, int32_t cols, int32_t tensor_rows, uint8_t* q, uint8_t* sf,

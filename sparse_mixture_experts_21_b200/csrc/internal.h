@@ -72,6 +72,13 @@ cudaError_t launch_ffn_f32(const float* x_rows, int64_t rows_cap, const int32_t*
                            const float* w1, const float* w3, const float* w2, int d, int f,
                            float* h, float* y, cudaStream_t s);
 
+// A whole layer for few tokens in one launch; w and sf: W1, W3, W2, shared W1, W3, W2.
+size_t few_workspace_bytes(const moe_config_t& c, int fs);
+cudaError_t launch_few(const moe_config_t& c, int64_t capacity, const void* x, const float* w_gate,
+                       const float* logit_offset, const float* bias, bool mxfp4, const void* const* w,
+                       const uint8_t* const* sf, int fs, int32_t* topk_idx, float* topk_w, void* y, void* ws,
+                       cudaStream_t s);
+
 cudaError_t launch_combine(const moe_config_t& c, const void* y_perm, const int32_t* row_of_slot,
                            const float* topk_w, const void* shared_out, const float* shared_w,
                            void* y, cudaStream_t s, const uint64_t* row_addr = nullptr);

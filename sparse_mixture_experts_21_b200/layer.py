@@ -323,6 +323,34 @@ class MoELayer:
         rec(6)
         return y
 
+    def forward_few(self, x: torch.Tensor, stream=None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """The layer for a few tokens (x [n, d], n <= 64, whatever the workload's T) in one
+        launch that reads only the picked experts' weights: a step of token-by-token
+        serving.  bf16, fp32 and MXFP4 experts; the picks are left in few_idx and few_w
+        [n, k].  With MXFP4 experts x and the hidden rows stay bf16 (forward quantises
+        them to MXFP8).  Writes no statistics and updates no bias.  Calls of one layer
+        share its scratch, so they must be ordered on the GPU; the first call allocates
+        it (make it before a capture)."""
+        w, W, n = self.w, self.weights, x.shape[0]
+        if w.expert_choice or w.fp8 or w.mxfp8 or w.nvfp4:
+            raise ValueError("forward_few runs token-choice routing over bf16, fp32 or MXFP4 experts")
+        if x.dim() != 2 or x.shape[1] != w.d or n > L.FEW_TOKENS_MAX:
+            raise ValueError(f"forward_few takes [n, {w.d}] with n <= {L.FEW_TOKENS_MAX}, not {list(x.shape)}")
+        if not hasattr(self, "_few"):
+            c = make_config(w, L.FEW_TOKENS_MAX)
+            self._few = {"ws": torch.empty(L.few_tokens_workspace_size(c, self.fs), dtype=torch.uint8, device=self.dev),
+                         "idx": torch.empty(L.FEW_TOKENS_MAX, w.k, dtype=torch.int32, device=self.dev),
+                         "w": torch.empty(L.FEW_TOKENS_MAX, w.k, device=self.dev), "cfg": {}}
+        B = self._few
+        c = B["cfg"].setdefault(n, make_config(w, n))
+        y = torch.empty_like(x) if out is None else out
+        self.few_idx, self.few_w = B["idx"][:n], B["w"][:n]
+        names = ("w1", "w3", "w2", "ws1", "ws3", "ws2")
+        fn, src = (L.moe_few_tokens_mxfp4, self.wq) if w.mxfp4 else (L.moe_few_tokens, W)
+        fn(c, x, W["w_gate"], W.get("logit_offset"), W.get("bias"), *(src.get(m) for m in names), self.fs,
+           self.few_idx, self.few_w, y, B["ws"], stream)
+        return y
+
     def _forward_ec(self, x, s, rec, y):
         """Expert-choice routing: scores -> per-expert top-C -> grouped FFN -> combine."""
         W, c, w = self.weights, self.cfg, self.w
