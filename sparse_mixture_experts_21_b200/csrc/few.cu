@@ -28,7 +28,6 @@
 // orders below what the pipes need to be the bound).  The order of k inside a fragment is
 // free as long as both operands use it, so a thread feeds the MMA with its own 16-byte
 // loads and no shuffles.
-#include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -45,6 +44,7 @@ constexpr int X_WARPS = 3;                      // warps that gather tokens' col
 constexpr int CONSUMERS = 32 * WARPS, THREADS = CONSUMERS + 32 + 32 * X_WARPS;
 constexpr int MAX_PASS = 32;                    // tokens of an expert per pass over its weights
 constexpr int SLOTS = 64;                       // weight rows of a stage
+constexpr int ROUTE_TILE = 16, ROUTE_COLS = 1024;   // router: experts and columns at a time
 enum { W_F32 = 0, W_BF16 = 1, W_MXFP4 = 2 };
 
 // The six expert stacks [experts * rows, cols]: W1, W3, W2 routed, then shared.
@@ -65,7 +65,7 @@ struct Args {
   void* y;
   unsigned* bar;           // two barrier counters, zero at launch
   unsigned* hmax;          // MXFP4: [T k + T] largest |h| of each row as bits, zero at launch
-  float* logits;           // [T, N + sink]
+  float* logits;           // [slices, T, N + sink] partial sums
   void* h;                 // [T k, f] routed, then [T, fs] shared; x's type
 };
 
@@ -111,6 +111,8 @@ template <int WT> __host__ __device__ constexpr int stage_bytes() {
 constexpr int RED_LD = SLOTS + 4;               // partial sums [token][row], padded: 32 banks
 template <int WT> __host__ __device__ constexpr int red_floats() { return Cfg<WT>::WK * 8 * RED_LD; }
 
+constexpr int RED_X_FLOATS = 8 * ROUTE_COLS;    // the router's tokens lie over the partial sums and the output tile
+
 // What selection leaves for the rest of the kernel.
 struct Tables {
   int16_t row0[MAX_N + 1];           // first row of each expert; rows of e: row0[e] .. row0[e + 1]
@@ -128,8 +130,8 @@ struct Tables {
 struct Scratch {
   int32_t idx[MAX_T * MAX_K];
   float w[MAX_T * MAX_K];
-  float lse[MAX_T];
   unsigned mask[MAX_N][2];           // tokens of each expert
+  int2 sums[WARPS];
 };
 constexpr int YACC_FLOATS = MAX_T * SLOTS;
 template <int WT> __host__ __device__ constexpr int smem_bytes() {
@@ -137,6 +139,9 @@ template <int WT> __host__ __device__ constexpr int smem_bytes() {
 }
 static_assert(smem_bytes<W_BF16>() <= 232448 && smem_bytes<W_F32>() <= 232448 && smem_bytes<W_MXFP4>() <= 232448,
               "shared memory per CTA");
+static_assert(WARPS * 2 * (MAX_N + 8) * 4 <= 3 * 43008, "scores in the ring");
+static_assert(RED_X_FLOATS <= 2 * red_floats<W_BF16>() + YACC_FLOATS && RED_X_FLOATS <= red_floats<W_MXFP4>() + YACC_FLOATS,
+              "router tokens");
 static_assert(sizeof(Scratch) <= (2 * red_floats<W_BF16>() + YACC_FLOATS) * 4, "selection scratch");
 
 // ------------------------------------------------------------------ waits
@@ -172,19 +177,174 @@ __device__ __forceinline__ void grid_wait(unsigned* bar, Tables& tb) {
 }
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(CONSUMERS) : "memory"); }
 
-// Selection for all T tokens by the CTA's warps (kept out of line: it needs more registers
-// than the rest of the kernel).
-template <int NV>
-__device__ __noinline__ void select_all(const float* logits, int ld, const rt::RouteArgs& a) {
-  float pacc[NV];
-  rt::select_tokens<NV, WARPS>(logits, ld, (int)a.T, 0, a, pacc);
+// ------------------------------------------------------------------ router
+// Logits in K slices: tiles of 16 experts (a warp each) by `slices` column ranges, spread over
+// the grid, so that a CTA reads a slice of x and not all of it.  Eight tokens at a time, their
+// columns in shared memory as fp32; partial sums to memory, added by the selection.
+__host__ __device__ __forceinline__ int route_tiles(int ld) { return (ld + ROUTE_TILE - 1) / ROUTE_TILE; }
+// At most 16 (the selection adds them one by one), at least 256 columns each, 144 jobs in all:
+// one for every SM of the grid.
+__host__ __device__ __forceinline__ int route_slices(int ld, int d) {
+  int n = 144 / route_tiles(ld), most = (d + 255) / 256;
+  n = n < most ? n : most;
+  return n < 1 ? 1 : n > 16 ? 16 : n;
+}
+__device__ __forceinline__ void load4(const float* p, float* f) { unpack16(ldg_nc16(p), f, 0.f); }
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, float* f) {
+  const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+  f[0] = __uint_as_float(v.x << 16); f[1] = __uint_as_float(v.x & 0xffff0000u);
+  f[2] = __uint_as_float(v.y << 16); f[3] = __uint_as_float(v.y & 0xffff0000u);
+}
+template <typename XT>
+__device__ __forceinline__ void router_logits(const Args& a, float4* xs) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int ld = a.N + a.sink, tiles = route_tiles(ld), slices = route_slices(ld, a.d);
+  const int quads = (a.d / 4 + slices - 1) / slices;
+  const XT* x = static_cast<const XT*>(a.x);
+  for (int job = blockIdx.x; job < tiles * slices; job += gridDim.x) {
+    const int s = job / tiles, e = (job - s * tiles) * ROUTE_TILE + warp;
+    const int q0 = s * quads, q1 = min(q0 + quads, a.d / 4);
+    const float* wg = a.w_gate + (size_t)min(e, ld - 1) * a.d;
+    for (int t0 = 0; t0 < a.T; t0 += 8) {
+      const int n = min(8, a.T - t0);
+      float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      for (int c0 = q0; c0 < q1; c0 += ROUTE_COLS / 4) {
+        const int nq = min(ROUTE_COLS / 4, q1 - c0);
+        float4 w[ROUTE_COLS / 128];
+#pragma unroll
+        for (int u = 0; u < ROUTE_COLS / 128; ++u)
+          w[u] = lane + 32 * u < nq ? __ldg(reinterpret_cast<const float4*>(wg) + c0 + lane + 32 * u)
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = tid; i < n * (ROUTE_COLS / 4); i += CONSUMERS) {
+          const int j = i / (ROUTE_COLS / 4), q = i % (ROUTE_COLS / 4);
+          float v[4] = {0.f, 0.f, 0.f, 0.f};
+          if (q < nq) load4(x + (size_t)(t0 + j) * a.d + 4 * (c0 + q), v);
+          xs[i] = make_float4(v[0], v[1], v[2], v[3]);
+        }
+        consumer_sync();
+        for (int j = 0; j < n; ++j) {
+          float p = 0.f;
+#pragma unroll
+          for (int u = 0; u < ROUTE_COLS / 128; ++u) {
+            const float4 v = xs[j * (ROUTE_COLS / 4) + lane + 32 * u];
+            p = fmaf(w[u].x, v.x, p);
+            p = fmaf(w[u].y, v.y, p);
+            p = fmaf(w[u].z, v.z, p);
+            p = fmaf(w[u].w, v.w, p);
+          }
+#pragma unroll
+          for (int m = 0; m < 8; ++m) acc[m] += m == j ? p : 0.f;
+        }
+        consumer_sync();
+      }
+      float mine = 0.f;                       // lane j: token t0 + j
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float v = warp_sum(acc[j]);
+        if (lane == j) mine = v;
+      }
+      if (lane < n && e < ld) a.logits[((size_t)s * a.T + t0 + lane) * ld + e] = mine;
+    }
+  }
+}
+
+// The next best of q[lo .. hi) after (key, index) in the order of falling key, then rising
+// index; index 0x7fffffff when none is left.
+__device__ __forceinline__ void next_best(const uint32_t* q, int lo, int hi, int lane, uint32_t& key, int& idx) {
+  uint32_t bk = 0;
+  int bi = 0x7fffffff;
+  for (int e = lo + lane; e < hi; e += 32) {
+    const uint32_t v = q[e];
+    if ((v < key || (v == key && e > idx)) && v > bk) { bk = v; bi = e; }
+  }
+  key = __reduce_max_sync(0xffffffffu, bk);
+  idx = (int)__reduce_min_sync(0xffffffffu, bk == key && bk > 0 ? (uint32_t)bi : 0x7fffffffu);
+}
+
+// Selection, a warp per token: moe_route's formulas, ties and order, in loops instead of
+// registers (a few tokens meet this code once, cold: its size counts more than its steps).
+// sv: the affinities, q: the selection scores as order-preserving keys (0: not eligible).
+__device__ __noinline__ void select_token(const Args& a, Tables& tb, Scratch& sc, int t, float* sv, uint32_t* q) {
+  const int lane = threadIdx.x & 31, N = a.N, k = a.k;
+  const int ld = N + a.sink, slices = route_slices(ld, a.d);
+  const rt::RouteArgs& r = a.route;
+  float m = -INFINITY;
+#pragma unroll 1
+  for (int e = lane; e < ld; e += 32) {
+    float z = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < slices; ++s) z += __ldcg(a.logits + ((size_t)s * a.T + t) * ld + e);
+    if (r.logit_offset && e < N) z += r.logit_offset[e];
+    sv[e] = z;
+    m = fmaxf(m, z);
+  }
+  m = warp_max(m);
+  const bool soft = r.score_fn == MOE_SCORE_SOFTMAX;
+  float se = 0.f;
+  if (soft) {
+#pragma unroll 1
+    for (int e = lane; e < ld; e += 32) se += expf(sv[e] - m);
+    se = warp_sum(se);
+  }
+#pragma unroll 1
+  for (int e = lane; e < ld; e += 32) {
+    const float z = sv[e];
+    const float s = soft ? expf(z - m) / se : 1.f / (1.f + expf(-z));
+    sv[e] = s;
+    if (e < N) q[e] = f32_key(r.bias ? s + r.bias[e] : s);
+  }
+  __syncwarp();
+  if (r.n_groups > 1) {
+    const int size = N / r.n_groups;
+    uint32_t mine = 0;                        // lane g: group g's score
+#pragma unroll 1
+    for (int g = 0; g < r.n_groups; ++g) {
+      uint32_t key = 0xffffffffu;
+      int idx = -1;
+      float sum = 0.f;
+#pragma unroll 1
+      for (int i = 0; i < r.group_topn; ++i) {
+        next_best(q, g * size, (g + 1) * size, lane, key, idx);
+        sum += key_f32(key);
+      }
+      if (lane == g) mine = f32_key(sum);
+    }
+    uint32_t kept = 0;
+#pragma unroll 1
+    for (int i = 0; i < r.topk_groups; ++i) {
+      const uint32_t v = lane < r.n_groups && !((kept >> lane) & 1u) ? mine : 0u;
+      const uint32_t best = __reduce_max_sync(0xffffffffu, v);
+      kept |= 1u << __reduce_min_sync(0xffffffffu, v == best && lane < r.n_groups && !((kept >> lane) & 1u) ? lane : 31);
+    }
+#pragma unroll 1
+    for (int g = 0; g < r.n_groups; ++g)
+      if (!((kept >> g) & 1u))
+        for (int e = g * size + lane; e < (g + 1) * size; e += 32) q[e] = 0;
+    __syncwarp();
+  }
+  uint32_t key = 0xffffffffu;
+  int idx = -1, my = 0x7fffffff;
+#pragma unroll 1
+  for (int j = 0; j < k; ++j) {
+    next_best(q, 0, N, lane, key, idx);
+    if (lane == j) my = idx;
+  }
+  const float s = lane < k && my < N ? sv[my] : 0.f;
+  const float sh = a.sink ? sv[N] : 0.f;
+  const float sum = warp_sum(s) + sh;
+  if (lane < k) {
+    sc.idx[t * k + lane] = my;
+    sc.w[t * k + lane] = r.renorm ? s / sum : s;
+  }
+  if (lane == 0 && a.sink) tb.shw[t] = r.renorm ? sh / sum : sh;
 }
 
 // Experts' token masks, met experts in ascending order, rows (expert major, tokens
-// ascending); a token past its expert's capacity gets no row.
+// ascending); a token past its expert's capacity gets no row.  A thread per expert.
+static_assert(CONSUMERS >= MAX_N, "a thread per expert");
 __device__ void build_tables(const Args& a, Tables& tb, Scratch& sc) {
-  const int tid = threadIdx.x, n = a.T * a.k;
-  for (int e = tid; e < a.N; e += CONSUMERS) sc.mask[e][0] = sc.mask[e][1] = 0;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = a.T * a.k;
+  if (tid < MAX_N) sc.mask[tid][0] = sc.mask[tid][1] = 0;
   consumer_sync();
   for (int s = tid; s < n; s += CONSUMERS) {
     const int e = sc.idx[s], t = s / a.k;
@@ -192,28 +352,30 @@ __device__ void build_tables(const Args& a, Tables& tb, Scratch& sc) {
     else flag_invalid_index();
   }
   consumer_sync();
-  if (tid < 32) {
-    int rows = 0, act = 0;
-    for (int base = 0; base < a.N; base += 32) {
-      const int e = base + tid;
-      int c = e < a.N ? __popc(sc.mask[e][0]) + __popc(sc.mask[e][1]) : 0;
-      if (c > a.capacity) c = (int)a.capacity;
-      int incl = c;
+  int c = tid < a.N ? __popc(sc.mask[tid][0]) + __popc(sc.mask[tid][1]) : 0;
+  if (c > a.capacity) c = (int)a.capacity;
+  int incl = c;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (tid >= o) incl += v;
-      }
-      const unsigned met = __ballot_sync(0xffffffffu, c > 0);
-      if (e < a.N) tb.row0[e + 1] = (int16_t)(rows + incl);
-      if (c > 0) tb.act[act + __popc(met & ((1u << tid) - 1u))] = (int16_t)e;
-      rows += __shfl_sync(0xffffffffu, incl, 31);
-      act += __popc(met);
-    }
-    if (tid == 0) {
-      tb.n_act = act;
-      tb.row0[0] = 0;
-    }
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  const unsigned met = __ballot_sync(0xffffffffu, c > 0);
+  if (lane == 31) sc.sums[warp] = make_int2(incl, __popc(met));
+  consumer_sync();
+  int rows = 0, act = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    const int2 v = sc.sums[w];
+    rows += w < warp ? v.x : 0;
+    act += w < warp ? v.y : 0;
+    all += v.y;
+  }
+  if (tid < a.N) tb.row0[tid + 1] = (int16_t)(rows + incl);
+  if (c > 0) tb.act[act + __popc(met & ((1u << lane) - 1u))] = (int16_t)tid;
+  if (tid == 0) {
+    tb.row0[0] = 0;
+    tb.n_act = all;
   }
   consumer_sync();
   for (int s = tid; s < n; s += CONSUMERS) {
@@ -226,8 +388,8 @@ __device__ void build_tables(const Args& a, Tables& tb, Scratch& sc) {
       tb.row_w[tb.row0[e] + below] = sc.w[s];
     }
   }
-  consumer_sync();
 }
+
 // ------------------------------------------------------------------ schedule
 // One pass over one tile of weight rows: at most 64 rows (gate/up: 32 hidden units, their
 // gate and up rows) by one expert's tokens, 32 at most.  Producers and consumers walk the
@@ -678,60 +840,6 @@ __device__ __forceinline__ void run_tile(const Args& a, Tables& tb, const Tile& 
   else run_pass<WT, DOWN, 4>(a, tb, t, r, stages, red, yacc, buf);
 }
 
-// Router logits of experts blockIdx.x, + grid, ...: two experts at a time, the warps splitting
-// the columns, eight tokens at a time.
-template <typename XT>
-__device__ __forceinline__ void load4(const XT* p, float* f);
-template <>
-__device__ __forceinline__ void load4(const float* p, float* f) { unpack16(ldg_nc16(p), f, 0.f); }
-template <>
-__device__ __forceinline__ void load4(const __nv_bfloat16* p, float* f) {
-  const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-  f[0] = __uint_as_float(v.x << 16); f[1] = __uint_as_float(v.x & 0xffff0000u);
-  f[2] = __uint_as_float(v.y << 16); f[3] = __uint_as_float(v.y & 0xffff0000u);
-}
-template <typename XT>
-__device__ __forceinline__ void router_logits(const Args& a, float* part) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, P = gridDim.x;
-  const int ld = a.N + a.sink;
-  const XT* x = static_cast<const XT*>(a.x);
-  for (int e0 = blockIdx.x; e0 < ld; e0 += 2 * P) {
-    const int ne = e0 + P < ld ? 2 : 1, slices = WARPS / ne;
-    const int e = e0 + (warp % ne) * P, slice = warp / ne;
-    const float* wg = a.w_gate + (size_t)e * a.d;
-    for (int t0 = 0; t0 < a.T; t0 += 8) {
-      const int n = min(8, a.T - t0);
-      float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
-      for (int c = (slice * 32 + lane) * 4; c < a.d; c += slices * 128) {
-        float w[4];
-        load4(wg + c, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (j >= n) break;
-          float v[4];
-          load4(x + (size_t)(t0 + j) * a.d + c, v);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[j] = fmaf(w[i], v[i], acc[j]);
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        acc[j] = warp_sum(acc[j]);
-        if (lane == 0) part[warp * 8 + j] = acc[j];
-      }
-      consumer_sync();
-      if (tid < ne * 8) {
-        const int i = tid >> 3, j = tid & 7;
-        float v = 0.f;
-        for (int s = 0; s < slices; ++s) v += part[(s * ne + i) * 8 + j];
-        if (j < n) a.logits[(size_t)(t0 + j) * ld + e0 + i * P] = v;
-      }
-      consumer_sync();
-    }
-  }
-}
-
 template <int WT>
 __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__ Args a,
                                                                const __grid_constant__ Maps maps) {
@@ -745,7 +853,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
   Tables& tb = *reinterpret_cast<Tables*>(yacc + YACC_FLOATS);
   Scratch& sc = *reinterpret_cast<Scratch*>(red);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int T = a.T, ld = a.N + a.sink;
+  const int T = a.T;
 
   if (tid == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
@@ -823,7 +931,8 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
     Ring r{0, 0};
     int buf = 0;
     Tile t;
-    router_logits<XT>(a, red);
+    router_logits<XT>(a, reinterpret_cast<float4*>(red));
+    consumer_sync();
     if (tid == 0) grid_arrive(a.bar);
     if (WT == W_MXFP4) {
       for (int tok = warp; tok < T; tok += WARPS) {
@@ -850,16 +959,13 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
     if (tid == 0) grid_wait(a.bar, tb);
     consumer_sync();
 
-    rt::RouteArgs ra = a.route;
-    ra.topk_idx = sc.idx;
-    ra.topk_w = sc.w;
-    ra.lse = sc.lse;
-    ra.shared_w = tb.shw;
-    if (a.N <= 32) select_all<1>(a.logits, ld, ra);
-    else if (a.N <= 64) select_all<2>(a.logits, ld, ra);
-    else if (a.N <= 128) select_all<4>(a.logits, ld, ra);
-    else if (a.N <= 256) select_all<8>(a.logits, ld, ra);
-    else select_all<16>(a.logits, ld, ra);
+    // the ring is empty now: it holds the warps' scores
+    {
+      float* sv = reinterpret_cast<float*>(smem) + warp * 2 * (MAX_N + 8);
+      for (int t0 = warp; t0 < T; t0 += WARPS)
+        select_token(a, tb, sc, t0, sv, reinterpret_cast<uint32_t*>(sv + MAX_N + 8));
+    }
+    fence_proxy_async();                   // before TMA writes there again
     consumer_sync();
     if (blockIdx.x == 0)
       for (int s = tid; s < T * a.k; s += CONSUMERS) {
@@ -928,7 +1034,10 @@ cudaError_t launch(const Args& a, const Maps& maps, size_t zero, cudaStream_t s)
 // Workspace, in this order: barrier counters and row maxima (zeroed by every call), logits,
 // hidden rows.
 size_t zero_bytes(const moe_config_t& c) { return align256(256 + (size_t)c.T * (c.top_k + 1) * 4); }
-size_t logit_bytes(const moe_config_t& c) { return align256((size_t)c.T * (c.n_experts + c.shared_sink) * 4); }
+size_t logit_bytes(const moe_config_t& c) {
+  const int ld = c.n_experts + c.shared_sink;
+  return align256((size_t)route_slices(ld, c.d_model) * c.T * ld * 4);
+}
 
 }  // namespace few
 

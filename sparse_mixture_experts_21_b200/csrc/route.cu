@@ -53,18 +53,16 @@ struct RouteArgs {
 // selection score once (stable, so the lower expert index stays first on ties), and
 // each of the k picks is one warp arg-max over the lanes' list heads, after which
 // the winning lane drops its head.  The margin is one more such round.
-//
-// select_tokens leaves each warp's sums of the normalised affinity over its tokens in
-// pacc; select_phase adds them over the block's warps.
 template <int NV, int WARPS>
-__device__ __forceinline__ void select_tokens(const float* logits, int ld, int TM, int64_t t0, const RouteArgs& a,
-                                              float (&pacc)[NV]) {
+__device__ void select_phase(const float* logits, int ld, int TM, int64_t t0, const RouteArgs& a,
+                             float* pwarp) {
   // each warp takes two tokens at a time (tm and tm + WARPS) through every step, so
   // the two tokens' dependent chains of warp reductions interleave (one token when a
   // lane holds more than 8 experts: the state of two would not fit in registers)
   constexpr int U = NV <= 8 ? 2 : 1;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int N = a.N, k = a.k;
+  float pacc[NV];
   // per-lane constants: validity, group of each column, bias and logit offset
   float bias_r[NV], off_r[NV];
   int gid[NV];
@@ -334,16 +332,6 @@ __device__ __forceinline__ void select_tokens(const float* logits, int ld, int T
       }
     }
   }
-
-}
-
-template <int NV, int WARPS>
-__device__ void select_phase(const float* logits, int ld, int TM, int64_t t0, const RouteArgs& a,
-                             float* pwarp) {
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int N = a.N;
-  float pacc[NV];
-  select_tokens<NV, WARPS>(logits, ld, TM, t0, a, pacc);
 
   // per-block sums of the normalised affinity, fixed order over warps
 #pragma unroll
