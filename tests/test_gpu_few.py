@@ -82,12 +82,20 @@ class Few:
             acc = w.d * 2.0 ** -24
             dh = 1.1 * acc * (np.abs(xe) @ np.abs(a).T) * np.abs(up) \
                 + np.abs(O.silu(gate)) * acc * (np.abs(xe) @ np.abs(b).T) + 2.0 ** -18 * np.abs(h)
-            dh = dh + u * (np.abs(h) + dh)
             f = c.shape[1]
+            dc = 0.0
+            if self.mxfp4:
+                # x and h as fp16 times a power of two that puts the row's largest at 2^14 or more: bf16's
+                # 8 bits are exact there but for what falls below half of fp16's smallest step, 2^-25:
+                # 2^-39 of the row's largest
+                ex = 2.0 ** -39 * np.abs(xe).max(1, keepdims=True)
+                dh = dh + ex * (1.1 * np.abs(up) * np.abs(a).sum(1) + np.abs(O.silu(gate)) * np.abs(b).sum(1))
+                dc = 2.0 ** -39 * (np.abs(h) + dh).max(1, keepdims=True) * np.abs(c).sum(1)
+            dh = dh + u * (np.abs(h) + dh)
             y[t] += g * (h @ c.T)
             # the down sum: f half-steps, and the weighting, the sum over experts and a shared
             # weight 2^-18 (up to k + 2 roundings of 2^-24 and the shared weight's own)
-            tol[t] += np.abs(g) * ((dh + (f * 2.0 ** -24 + 2.0 ** -18) * (np.abs(h) + dh)) @ np.abs(c).T)
+            tol[t] += np.abs(g) * ((dh + (f * 2.0 ** -24 + 2.0 ** -18) * (np.abs(h) + dh)) @ np.abs(c).T + dc)
         return y, tol + u * (np.abs(y) + tol)
 
     def check(self, routing=True):
