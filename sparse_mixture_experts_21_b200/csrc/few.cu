@@ -180,37 +180,23 @@ struct Gather {
 };
 
 // ------------------------------------------------------------------ products
-__device__ __forceinline__ uint4 lds16(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds4(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds1(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds2(uint32_t a) {
-  uint32_t v;
-  asm volatile("{\n\t.reg .u16 h;\n\tld.shared.u16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(v) : "r"(a));
-  return v;
-}
+// Plain loads and MMAs without side effects: the compiler may move a tile's loads over the
+// products before them.
+__device__ __forceinline__ uint4 lds16(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
+__device__ __forceinline__ uint32_t lds4(const uint8_t* p) { return *reinterpret_cast<const uint32_t*>(p); }
+__device__ __forceinline__ uint32_t lds2(const uint8_t* p) { return *reinterpret_cast<const uint16_t*>(p); }
+__device__ __forceinline__ uint32_t lds1(const uint8_t* p) { return *p; }
 // D += A B, 16 x 8 x 16, fp32 accumulators: rows g and g + 8, columns 2t and 2t + 1 of lane 4g + t.
 __device__ __forceinline__ void mma_bf16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 // D = A B + C in fp16.
 __device__ __forceinline__ void mma_f16(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1, float c0, float c1, float c2, float c3) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
                : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
@@ -257,12 +243,12 @@ struct Product {
 #pragma unroll
     for (int i = 0; i < NT * 4; ++i) acc[0][i] = 0.f;
   }
-  __device__ __forceinline__ void stage(const Tile& t, int k0, uint32_t st, int warp, int lane) {
+  __device__ __forceinline__ void stage(const Tile& t, int k0, const uint8_t* st, int warp, int lane) {
     constexpr int SEG = C::seg(NT), WS = wstride<C>(NT), XS = xstride<C>(NT);
     const int q = warp & 3, kq = warp >> 2, g = lane >> 2, tq = lane & 3;
     if ((DOWN ? 2 : 1) * q >= t.nu) return;
     const int cols = t.K - k0;
-    const uint32_t wa = st + (16 * q + g) * WS, xa = st + SLOTS * WS + g * XS;
+    const uint8_t *wa = st + (16 * q + g) * WS, *xa = st + SLOTS * WS + g * XS;
 #pragma unroll
     for (int kk = 0; kk < SEG / 4; kk += 32) {
       const int c = kq * (SEG / 4) + kk + 8 * tq;
@@ -294,12 +280,12 @@ struct Product<float, DOWN, NT> {
 #pragma unroll
     for (int i = 0; i < 2 * NT * 8; ++i) acc[0][0][i] = 0.f;
   }
-  __device__ __forceinline__ void stage(const Tile& t, int k0, uint32_t st, int warp, int lane) {
+  __device__ __forceinline__ void stage(const Tile& t, int k0, const uint8_t* st, int warp, int lane) {
     constexpr int SEG = C::seg(NT), WS = wstride<C>(NT), XS = xstride<C>(NT);
     const int q = warp & 3, kq = warp >> 2, g = lane >> 2, tq = lane & 3;
     if ((DOWN ? 2 : 1) * q >= t.nu) return;
     const int cols = t.K - k0;
-    const uint32_t wa = st + (16 * q + g) * WS, xa = st + SLOTS * WS;
+    const uint8_t *wa = st + (16 * q + g) * WS, *xa = st + SLOTS * WS;
 #pragma unroll 1
     for (int kk = 0; kk < SEG / 4; kk += 16) {
       const int c = kq * (SEG / 4) + kk + 4 * tq;
@@ -355,16 +341,16 @@ struct Product<Mxfp4, DOWN, NT> {
 #pragma unroll
     for (int n = 0; n < NT; ++n) ts[n] = 8 * n + (lane >> 2) < t.n ? token_scale<DOWN>(t, tb, 8 * n + (lane >> 2)) : 0.f;
   }
-  __device__ __forceinline__ void stage(const Tile& t, int k0, uint32_t st, int warp, int lane) {
+  __device__ __forceinline__ void stage(const Tile& t, int k0, const uint8_t* st, int warp, int lane) {
     constexpr int SEG = C::seg(NT), WS = wstride<C>(NT), XS = xstride<C>(NT), BLOCKS = SEG / WARPS / 32;
     const int g = lane >> 2, tq = lane & 3;
     const int c0 = warp * (SEG / WARPS);
     if (c0 >= t.K - k0) return;              // whole 128-column blocks: uniform over the warp
     // 64-byte chunk c0 / 128 of the group's rows; its 16-byte unit (c0 / 32) % 4, swizzled
     const int unit = (c0 >> 5) & 3;
-    const uint32_t wa = st + 512 * (c0 >> 7) + 64 * g + 4 * tq;
-    const uint32_t xa = st + SLOTS * WS + g * XS + 16 * tq + 2 * c0;
-    const uint32_t sa = st + SLOTS * WS + 8 * NT * XS + SF_LD * g + (c0 >> 5);
+    const uint8_t *wa = st + 512 * (c0 >> 7) + 64 * g + 4 * tq;
+    const uint8_t* xa = st + SLOTS * WS + g * XS + 16 * tq + 2 * c0;
+    const uint8_t* sa = st + SLOTS * WS + 8 * NT * XS + SF_LD * g + (c0 >> 5);
     uint32_t b[BLOCKS][NT][4];
 #pragma unroll
     for (int k = 0; k < BLOCKS; ++k)
@@ -376,7 +362,7 @@ struct Product<Mxfp4, DOWN, NT> {
         b[k][n][2] = scaled_f16(v.z, ts[n]);
         b[k][n][3] = scaled_f16(v.w, ts[n]);
       }
-    uint32_t wu[BLOCKS];
+    const uint8_t* wu[BLOCKS];
 #pragma unroll
     for (int k = 0; k < BLOCKS; ++k) wu[k] = wa + 16 * ((unit + k) ^ ((g >> 1) & 3));
 #pragma unroll
@@ -416,7 +402,7 @@ struct Product<Mxfp4, DOWN, NT> {
 // One tile pass: all its stages, then the warps' partial sums through shared memory and the
 // tile's results.  gate/up: h = silu(gate) * up to memory; down: weighted sums into yacc.
 template <typename W, bool DOWN, int NT>
-__device__ __forceinline__ void run_pass(const Args& a, Tables& tb, const Tile& t, Ring& r, uint32_t stages, float* red,
+__device__ __forceinline__ void run_pass(const Args& a, Tables& tb, const Tile& t, Ring& r, const uint8_t* stages, float* red,
                                          float* yacc, int& buf) {
   using C = Cfg<W>;
   using XT = typename C::XT;
@@ -492,7 +478,7 @@ __device__ __forceinline__ void run_pass(const Args& a, Tables& tb, const Tile& 
 }
 
 template <typename W, bool DOWN>
-__device__ __forceinline__ void run_tile(const Args& a, Tables& tb, const Tile& t, Ring& r, uint32_t stages, float* red,
+__device__ __forceinline__ void run_tile(const Args& a, Tables& tb, const Tile& t, Ring& r, const uint8_t* stages, float* red,
                                          float* yacc, int& buf) {
   if (t.nt == 1) run_pass<W, DOWN, 1>(a, tb, t, r, stages, red, yacc, buf);
   else if (t.nt == 2) run_pass<W, DOWN, 2>(a, tb, t, r, stages, red, yacc, buf);
@@ -606,9 +592,9 @@ few_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps) {
       worker_sync();
     }
     if (a.fs > 0)
-      for (Gate w(a, tb, true); w.next(t);) run_tile<W, false>(a, tb, t, r, stages, red, yacc, buf);
+      for (Gate w(a, tb, true); w.next(t);) run_tile<W, false>(a, tb, t, r, smem, red, yacc, buf);
     __syncthreads();                       // the tables are there
-    for (Gate w(a, tb, false); w.next(t);) run_tile<W, false>(a, tb, t, r, stages, red, yacc, buf);
+    for (Gate w(a, tb, false); w.next(t);) run_tile<W, false>(a, tb, t, r, smem, red, yacc, buf);
     // this CTA's hidden rows to the grid
     __threadfence();
     worker_sync();
@@ -632,7 +618,7 @@ few_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps) {
         y[i] = (XT)0.f;
     }
     while (w.next(t)) {
-      run_tile<W, true>(a, tb, t, r, stages, red, yacc, buf);
+      run_tile<W, true>(a, tb, t, r, smem, red, yacc, buf);
       if (!t.last) continue;
       worker_sync();
       for (int i = tid; i < T * SLOTS; i += CONSUMERS) {

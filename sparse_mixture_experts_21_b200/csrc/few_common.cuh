@@ -39,6 +39,7 @@ struct Args {
 };
 
 // The selecting warp's.
+constexpr int PART = 1536;           // partial sums of logits at a time
 struct Scratch {
   union {
     struct {
@@ -47,10 +48,17 @@ struct Scratch {
     };
     float w[MAX_T * MAX_K];          // then all picks' weights
   };
-  float wl[LOCAL_T * MAX_K];         // picks' weights of one or two tokens
-  int16_t e[MAX_T * MAX_K];          // picks
-  unsigned mask[MAX_N][2];           // tokens of each expert
+  union {
+    float part[PART];
+    struct {
+      int16_t e[MAX_T * MAX_K];      // then all picks
+      unsigned mask[MAX_N][2];       // tokens of each expert
+    };
+  };
+  float wl[LOCAL_T * MAX_K];         // picks of one or two tokens
+  int16_t el[LOCAL_T * MAX_K];
 };
+static_assert(PART >= MAX_N + 4, "a slice at a time");
 // What selection leaves for the rest of the kernel.
 struct Tables {
   int16_t row0[MAX_N + 1];           // first row of each expert; rows of e: row0[e] .. row0[e + 1]
@@ -116,6 +124,8 @@ __host__ __device__ __forceinline__ int route_slices(int ld, int d) {
   n = n < 16 ? n : 16;
   return n > least ? n : least;
 }
+// Floats between the rows of the partial sums: a row is copied 16 bytes at a time.
+__host__ __device__ __forceinline__ int route_ld(int ld) { return (ld + 3) & ~3; }
 __device__ __forceinline__ void ldg_quad(const float* p, uint4& v) { v = ldg_nc16(p); }
 __device__ __forceinline__ void ldg_quad(const __nv_bfloat16* p, uint2& v) {
   v = __ldg(reinterpret_cast<const uint2*>(p));
@@ -177,7 +187,7 @@ __device__ __forceinline__ void router_logits(const Args& a, float4* xs) {
         p = warp_sum(p);
         if (lane == j) mine = p;
       }
-      if (lane < n && e < ld) a.logits[((size_t)s * a.T + t0 + lane) * ld + e] = mine;
+      if (lane < n && e < ld) a.logits[((size_t)s * a.T + t0 + lane) * route_ld(ld) + e] = mine;
       worker_sync();
     }
   }
@@ -205,34 +215,33 @@ __device__ __noinline__ void select_token(const Args& a, Tables& tb, int t) {
   const int lane = threadIdx.x & 31, N = a.N, k = a.k;
   const int ld = N + a.sink, slices = route_slices(ld, a.d);
   const rt::RouteArgs& r = a.route;
+  // the slices' sums, through shared memory: one wait for as many as fit
+  const int ldp = route_ld(ld), per = PART / ldp;
+#pragma unroll 1
+  for (int s0 = 0; s0 < slices; s0 += per) {
+    const int n = min(per, slices - s0);
+#pragma unroll 1
+    for (int s = 0; s < n; ++s) {
+      const float* src = a.logits + ((size_t)(s0 + s) * a.T + t) * ldp;
+#pragma unroll 1
+      for (int c = 4 * lane; c < ldp; c += 128) cp_async16(smem_u32(sc.part + s * ldp + c), src + c);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+#pragma unroll 1
+    for (int e = lane; e < ld; e += 32) {
+      float z = s0 ? sv[e] : 0.f;
+#pragma unroll 4
+      for (int s = 0; s < n; ++s) z += sc.part[s * ldp + e];
+      sv[e] = z;
+    }
+    __syncwarp();
+  }
   float m = -INFINITY;
 #pragma unroll 1
-  for (int e0 = lane; e0 < ld; e0 += 128) {
-    // four experts by sixteen slices at a time: the loads are in flight together (one wait, not
-    // one per slice, under a memory system that the weights' stream keeps full)
-    float z[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-    for (int s0 = 0; s0 < slices; s0 += 16) {
-      float v[16][4];
-#pragma unroll
-      for (int s = 0; s < 16; ++s)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          v[s][i] = s0 + s < slices && e0 + 32 * i < ld
-                        ? __ldcg(a.logits + ((size_t)(s0 + s) * a.T + t) * ld + e0 + 32 * i) : 0.f;
-#pragma unroll
-      for (int s = 0; s < 16; ++s)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) z[i] += v[s][i];
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int e = e0 + 32 * i;
-      if (e >= ld) break;
-      if (r.logit_offset && e < N) z[i] += r.logit_offset[e];
-      sv[e] = z[i];
-      m = fmaxf(m, z[i]);
-    }
+  for (int e = lane; e < ld; e += 32) {
+    if (r.logit_offset && e < N) sv[e] += r.logit_offset[e];
+    m = fmaxf(m, sv[e]);
   }
   m = warp_max(m);
   const bool soft = r.score_fn == MOE_SCORE_SOFTMAX;
@@ -305,7 +314,7 @@ __device__ __noinline__ void select_token(const Args& a, Tables& tb, int t) {
   // the CTA that owns the token writes the outputs
   if (lane < k) {
     if (a.T <= LOCAL_T) {
-      sc.e[t * k + lane] = (int16_t)my;
+      sc.el[t * k + lane] = (int16_t)my;
       sc.wl[t * k + lane] = w;
     }
     if (t % (int)gridDim.x == (int)blockIdx.x) {
@@ -326,7 +335,13 @@ __device__ __noinline__ void build_tables(const Args& a, Tables& tb) {
   Scratch& sc = tb.sc;
   const int lane = threadIdx.x & 31, n = a.T * a.k;
   for (int e = lane; e < a.N; e += 32) sc.mask[e][0] = sc.mask[e][1] = 0;
-  if (a.T > LOCAL_T) {                        // the picks that the grid wrote
+  if (a.T <= LOCAL_T) {
+    if (lane < n) {
+      const int e = sc.el[lane];
+      sc.e[lane] = (unsigned)e < (unsigned)a.N ? (int16_t)e : (int16_t)-1;
+      sc.w[lane] = sc.wl[lane];
+    }
+  } else {                                    // the picks that the grid wrote
 #pragma unroll 4
     for (int s = lane; s < n; s += 32) {
       const int e = __ldcg(a.topk_idx + s);
@@ -376,7 +391,7 @@ __device__ __noinline__ void build_tables(const Args& a, Tables& tb) {
                                   : __popc(sc.mask[e][0]) + __popc(sc.mask[e][1] & ((1u << (t - 32)) - 1u));
     if ((int64_t)below < a.capacity) {
       tb.row_tok[tb.row0[e] + below] = (uint8_t)t;
-      tb.row_w[tb.row0[e] + below] = a.T > LOCAL_T ? sc.w[s] : sc.wl[s];
+      tb.row_w[tb.row0[e] + below] = sc.w[s];
     }
   }
 }
@@ -497,7 +512,7 @@ size_t zero_bytes(const moe_config_t& c) { return align256(256 + (size_t)c.T * (
 size_t shw_bytes(const moe_config_t& c) { return align256((size_t)c.T * 4); }
 size_t logit_bytes(const moe_config_t& c) {
   const int ld = c.n_experts + c.shared_sink;
-  return align256((size_t)route_slices(ld, c.d_model) * c.T * ld * 4);
+  return align256((size_t)route_slices(ld, c.d_model) * c.T * route_ld(ld) * 4);
 }
 
 }  // namespace few
