@@ -120,6 +120,18 @@ __device__ __forceinline__ void issue_w(const CUtensorMap* ma, const CUtensorMap
 __device__ __forceinline__ void cp_async4(uint32_t smem_dst, const void* gsrc) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_dst), "l"(gsrc) : "memory");
 }
+// With 8 tokens or fewer, the down pass gives every token its own column whatever the expert:
+// a warp then keeps the weighted sum over the experts in its registers and the warps' sums
+// meet once a tile instead of once an expert.  Row of token c of the expert, or -1.
+__device__ __forceinline__ bool by_token(const Args& a) { return a.T <= 8; }
+__device__ __forceinline__ int row_of_token(const Tables& tb, const Tile& t, int c) {
+  if (t.sh) return c < t.n ? c : -1;
+  int r = -1;
+  for (int i = 0; i < t.n; ++i)
+    if (tb.row_tok[t.row + i] == c) r = i;
+  return r;
+}
+
 // The token warps' part of a pass, set up once per tile so that a stage costs few instructions
 // (each is a warp's dependent step of five cycles or so, against the ~700 to 1400 cycles that
 // a stage takes from HBM): the same columns of the pass's tokens (x gathered by token, or
@@ -144,8 +156,11 @@ struct Gather {
     xs_ld = C::EB * t.seg + 64;
     xs = SLOTS * C::wbytes(t.seg);
 #pragma unroll
-    for (int m = 0; m < NTOK; ++m)
-      tok[m] = xw + X_WARPS * m < t.n ? token(a, tb, t, xw + X_WARPS * m) + 16 * lane : nullptr;
+    for (int m = 0; m < NTOK; ++m) {
+      const int c = xw + X_WARPS * m;            // the stage's token row
+      const int i = DOWN && by_token(a) ? row_of_token(tb, t, c) : c < t.n ? c : -1;
+      tok[m] = i >= 0 ? token(a, tb, t, i) + 16 * lane : nullptr;
+    }
     xs += xw * xs_ld + 16 * lane;
     if (C::MX) {
       const int s0 = 4 * xw + (lane >> 3), kb = lane & 7;
@@ -234,14 +249,25 @@ __device__ __forceinline__ float token_scale(const Tile& t, const Tables& tb, in
 
 // This warp's sums over a pass: a 16-row tile by 8 NT tokens on its share of the columns.
 // result(q, n, c): 16-row tile q of the warp's, column n, laid out as mma.sync's accumulators.
+// fold: adds the pass, times the weights of its columns' tokens, to the sum over passes, for
+// the columns (of this lane's two) that hold a token: a weight that is not a number stays with
+// its own expert's tokens.  cols: bits of the columns that hold a token.
 template <typename W, bool DOWN, int NT>
 struct Product {
   using C = Cfg<W>;
   static constexpr int QT = 1;
-  float acc[NT][4];
-  __device__ __forceinline__ void init(const Tile&, const Tables&, int) {
+  float acc[NT][4], sum[1][4] = {};
+  bool on[NT];                             // column 8 n + g
+  __device__ __forceinline__ void init(const Tile&, const Tables&, int lane, uint32_t cols) {
 #pragma unroll
     for (int i = 0; i < NT * 4; ++i) acc[0][i] = 0.f;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) on[n] = (cols >> (8 * n + (lane >> 2))) & 1u;
+  }
+  __device__ __forceinline__ void fold(float w0, float w1, bool on0, bool on1, int) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i & 1 ? on1 : on0) sum[0][i] = fmaf(i & 1 ? w1 : w0, acc[0][i], sum[0][i]);
   }
   __device__ __forceinline__ void stage(const Tile& t, int k0, const uint8_t* st, int warp, int lane) {
     constexpr int SEG = C::seg(NT), WS = wstride<C>(NT), XS = xstride<C>(NT);
@@ -257,7 +283,7 @@ struct Product {
       const uint4 a0 = ok ? lds16(wa + 2 * c) : z, a1 = ok ? lds16(wa + 8 * WS + 2 * c) : z;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const uint4 b = ok ? lds16(xa + n * 8 * XS + 2 * c) : z;
+        const uint4 b = ok && on[n] ? lds16(xa + n * 8 * XS + 2 * c) : z;
         mma_bf16(acc[n], a0.x, a1.x, a0.y, a1.y, b.x, b.y);
         mma_bf16(acc[n], a0.z, a1.z, a0.w, a1.w, b.z, b.w);
       }
@@ -275,10 +301,19 @@ template <bool DOWN, int NT>
 struct Product<float, DOWN, NT> {
   using C = Cfg<float>;
   static constexpr int QT = 1;
-  float acc[2][NT][8];
-  __device__ __forceinline__ void init(const Tile&, const Tables&, int) {
+  float acc[2][NT][8], sum[1][4] = {};
+  uint32_t on;
+  __device__ __forceinline__ void init(const Tile&, const Tables&, int, uint32_t cols) {
 #pragma unroll
     for (int i = 0; i < 2 * NT * 8; ++i) acc[0][0][i] = 0.f;
+    on = cols;
+  }
+  __device__ __forceinline__ void fold(float w0, float w1, bool on0, bool on1, int lane) {
+    float c[4];
+    result(0, 0, lane, c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i & 1 ? on1 : on0) sum[0][i] = fmaf(i & 1 ? w1 : w0, c[i], sum[0][i]);
   }
   __device__ __forceinline__ void stage(const Tile& t, int k0, const uint8_t* st, int warp, int lane) {
     constexpr int SEG = C::seg(NT), WS = wstride<C>(NT), XS = xstride<C>(NT);
@@ -297,6 +332,7 @@ struct Product<float, DOWN, NT> {
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
+          if (!((on >> (8 * n + j)) & 1u)) continue;
           float x[4];
           unpack16(lds16(xa + (8 * n + j) * XS + 4 * c), x, 0.f);
 #pragma unroll
@@ -333,13 +369,24 @@ template <bool DOWN, int NT>
 struct Product<Mxfp4, DOWN, NT> {
   using C = Cfg<Mxfp4>;
   static constexpr int QT = 4;
-  float acc[4][NT][4];
-  float ts[NT];                            // scale of token 8 n + g
-  __device__ __forceinline__ void init(const Tile& t, const Tables& tb, int lane) {
+  float acc[4][NT][4], sum[DOWN && NT == 1 ? 4 : 1][4] = {};
+  float ts[NT];                            // scale of column 8 n + g's token; 0: none
+  __device__ __forceinline__ void init(const Tile& t, const Tables& tb, int lane, uint32_t) {
 #pragma unroll
     for (int i = 0; i < 4 * NT * 4; ++i) acc[0][0][i] = 0.f;
 #pragma unroll
     for (int n = 0; n < NT; ++n) ts[n] = 8 * n + (lane >> 2) < t.n ? token_scale<DOWN>(t, tb, 8 * n + (lane >> 2)) : 0.f;
+  }
+  // columns by token: row i (or -1) of column g
+  __device__ __forceinline__ void scale_of(const Tile& t, const Tables& tb, int i) {
+    ts[0] = i >= 0 ? token_scale<DOWN>(t, tb, i) : 0.f;
+  }
+  __device__ __forceinline__ void fold(float w0, float w1, bool on0, bool on1, int) {
+#pragma unroll
+    for (int q = 0; q < (DOWN && NT == 1 ? 4 : 1); ++q)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i & 1 ? on1 : on0) sum[q][i] = fmaf(i & 1 ? w1 : w0, acc[q][0][i], sum[q][i]);
   }
   __device__ __forceinline__ void stage(const Tile& t, int k0, const uint8_t* st, int warp, int lane) {
     constexpr int SEG = C::seg(NT), WS = wstride<C>(NT), XS = xstride<C>(NT), BLOCKS = SEG / WARPS / 32;
@@ -357,10 +404,11 @@ struct Product<Mxfp4, DOWN, NT> {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const uint4 v = lds16(xa + n * 8 * XS + 64 * k);
-        b[k][n][0] = scaled_f16(v.x, ts[n]);
-        b[k][n][1] = scaled_f16(v.y, ts[n]);
-        b[k][n][2] = scaled_f16(v.z, ts[n]);
-        b[k][n][3] = scaled_f16(v.w, ts[n]);
+        // a column without a token holds whatever the stage held before: zeros instead
+        b[k][n][0] = ts[n] > 0.f ? scaled_f16(v.x, ts[n]) : 0u;
+        b[k][n][1] = ts[n] > 0.f ? scaled_f16(v.y, ts[n]) : 0u;
+        b[k][n][2] = ts[n] > 0.f ? scaled_f16(v.z, ts[n]) : 0u;
+        b[k][n][3] = ts[n] > 0.f ? scaled_f16(v.w, ts[n]) : 0u;
       }
     const uint8_t* wu[BLOCKS];
 #pragma unroll
@@ -408,7 +456,7 @@ __device__ __forceinline__ void run_pass(const Args& a, Tables& tb, const Tile& 
   using XT = typename C::XT;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   Product<W, DOWN, NT> p;
-  p.init(t, tb, lane);
+  p.init(t, tb, lane, t.n < 32 ? (1u << t.n) - 1u : 0xffffffffu);
   for (int k0 = 0; k0 < t.K; k0 += C::seg(NT)) {
     wait(&tb.full[r.stage], r.phase, tb);
     p.stage(t, k0, stages + r.stage * stage_bytes<C>(), warp, lane);
@@ -478,11 +526,70 @@ __device__ __forceinline__ void run_pass(const Args& a, Tables& tb, const Tile& 
 }
 
 template <typename W, bool DOWN>
-__device__ __forceinline__ void run_tile(const Args& a, Tables& tb, const Tile& t, Ring& r, const uint8_t* stages, float* red,
-                                         float* yacc, int& buf) {
+__device__ __forceinline__ void run_tile(const Args& a, Tables& tb, const Tile& t, Ring& r, const uint8_t* stages,
+                                         float* red, float* yacc, int& buf) {
   if (t.nt == 1) run_pass<W, DOWN, 1>(a, tb, t, r, stages, red, yacc, buf);
   else if (t.nt == 2) run_pass<W, DOWN, 2>(a, tb, t, r, stages, red, yacc, buf);
   else run_pass<W, DOWN, 4>(a, tb, t, r, stages, red, yacc, buf);
+}
+
+// Down with 8 tokens or fewer: all passes of a tile, columns by token, one meeting at the end.
+// w: at the tile's first pass; t: its passes in turn.
+template <typename W>
+__device__ __forceinline__ void run_down_by_token(const Args& a, Tables& tb, Walk<Cfg<W>, true>& w, Ring& r,
+                                                  const uint8_t* stages, float* red) {
+  using C = Cfg<W>;
+  using XT = typename C::XT;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, T = a.T;
+  XT* y = static_cast<XT*>(a.y);
+  Product<W, true, 1> p;
+  Tile t;
+  while (w.next(t)) {
+    // this lane's tokens: column g of the operand, columns 2 tq and 2 tq + 1 of the result
+    uint32_t cols = 0;
+    float w0 = 0.f, w1 = 0.f;
+    int mine = -1;
+    for (int i = 0; i < t.n; ++i) {
+      const int tok = t.sh ? i : tb.row_tok[t.row + i];
+      float v = t.sh ? tb.shw[tok] : tb.row_w[t.row + i];
+      if (C::MX) v *= inverse_pow2(token_scale<true>(t, tb, i));
+      cols |= 1u << tok;
+      if (tok == 2 * (lane & 3)) w0 = v;
+      if (tok == 2 * (lane & 3) + 1) w1 = v;
+      if (tok == (lane >> 2)) mine = i;
+    }
+    p.init(t, tb, lane, cols);
+    if constexpr (C::MX) p.scale_of(t, tb, mine);
+    for (int k0 = 0; k0 < t.K; k0 += C::seg(1)) {
+      wait(&tb.full[r.stage], r.phase, tb);
+      p.stage(t, k0, stages + r.stage * stage_bytes<C>(), warp, lane);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tb.empty[r.stage]);
+      r.next(C::STAGES);
+    }
+    p.fold(w0, w1, (cols >> (2 * (lane & 3))) & 1u, (cols >> (2 * (lane & 3) + 1)) & 1u, lane);
+    if (!t.last) continue;
+    const int wk = p.QT == 4 ? warp : warp >> 2;
+#pragma unroll
+    for (int q = 0; q < p.QT; ++q) {
+      float* o = red + (wk * 8 + 2 * (lane & 3)) * RED_LD + 16 * (p.QT == 4 ? q : warp & 3) + (lane >> 2);
+      o[0] = p.sum[q][0];
+      o[RED_LD] = p.sum[q][1];
+      o[8] = p.sum[q][2];
+      o[RED_LD + 8] = p.sum[q][3];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p.sum[q][i] = 0.f;
+    }
+    worker_sync();
+    const int tok = tid >> 6, j = slot_row<true>(t, tid & 63);
+    if (tok < T && j >= 0) {
+      float v = 0.f;
+#pragma unroll
+      for (int k = 0; k < C::WK; ++k) v += red[(k * 8 + tok) * RED_LD + (tid & 63)];
+      y[(size_t)tok * a.d + j] = (XT)v;
+    }
+    worker_sync();
+  }
 }
 
 template <typename W>
@@ -617,6 +724,7 @@ few_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps) {
       for (size_t i = (size_t)blockIdx.x * CONSUMERS + tid; i < (size_t)T * a.d; i += (size_t)gridDim.x * CONSUMERS)
         y[i] = (XT)0.f;
     }
+    if (by_token(a)) run_down_by_token<W>(a, tb, w, r, smem, red);
     while (w.next(t)) {
       run_tile<W, true>(a, tb, t, r, smem, red, yacc, buf);
       if (!t.last) continue;

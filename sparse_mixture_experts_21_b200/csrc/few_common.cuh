@@ -262,6 +262,26 @@ __device__ __noinline__ void select_token(const Args& a, Tables& tb, int t) {
   if (r.n_groups > 1) {
     const int size = N / r.n_groups;
     uint32_t mine = 0;                        // lane g: group g's score
+    const int per = 32 / r.n_groups;
+    if (r.group_topn <= 2 && per * r.n_groups == 32) {
+      // the usual case, all groups at once: `per` lanes each keep a group's two best, then merge
+      const int g = lane / per;
+      uint32_t k1 = 0, k2 = 0;
+#pragma unroll 1
+      for (int e = g * size + lane % per; e < (g + 1) * size; e += per) {
+        const uint32_t v = q[e];
+        k2 = max(k2, min(k1, v));
+        k1 = max(k1, v);
+      }
+#pragma unroll 1
+      for (int o = 1; o < per; o <<= 1) {
+        const uint32_t o1 = __shfl_xor_sync(0xffffffffu, k1, o), o2 = __shfl_xor_sync(0xffffffffu, k2, o);
+        k2 = max(max(k2, o2), min(k1, o1));
+        k1 = max(k1, o1);
+      }
+      const uint32_t score = f32_key(r.group_topn == 1 ? 0.f + key_f32(k1) : key_f32(k1) + key_f32(k2));
+      mine = __shfl_sync(0xffffffffu, score, (lane % r.n_groups) * per);
+    } else {
 #pragma unroll 1
     for (int g = 0; g < r.n_groups; ++g) {
       uint32_t key = 0xffffffffu;
@@ -273,6 +293,7 @@ __device__ __noinline__ void select_token(const Args& a, Tables& tb, int t) {
         sum += key_f32(key);
       }
       if (lane == g) mine = f32_key(sum);
+    }
     }
     uint32_t kept = 0;
 #pragma unroll 1

@@ -247,6 +247,26 @@ def test_weight_blocks_that_are_nan():
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp32", "mxfp4"])
+@pytest.mark.parametrize("T", [2, 7, 12])
+def test_an_expert_that_is_nan_spoils_only_its_own_tokens(kind, T):
+    w = replace(V3, T=T, N=16, k=2, n_groups=1, n_shared=0, bias_std=0.0, dtype="fp32" if kind == "fp32" else "bf16")
+    inp = make_inputs(w, "cuda", 6)
+    few = Few(w, mxfp4=kind == "mxfp4", inp=inp)
+    few.call()
+    torch.cuda.synchronize()
+    want, idx = few.y[:T].clone(), few.idx[:T].clone()
+    e = int(idx[0, 0])
+    for name in ("w1", "w2"):
+        inp[name][e] = float("nan")
+    few = Few(w, mxfp4=kind == "mxfp4", inp=inp)
+    few.call()
+    torch.cuda.synchronize()
+    hit = (idx == e).any(1)
+    assert hit.any() and not hit.all()
+    assert torch.isnan(few.y[:T][hit]).all() and torch.equal(few.y[:T][~hit], want[~hit])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32", "mxfp4"])
 def test_same_bits_every_time_and_on_another_stream(kind):
     few = Few(replace(V3, T=23, dtype="fp32" if kind == "fp32" else "bf16"), mxfp4=kind == "mxfp4")
     few.call()
