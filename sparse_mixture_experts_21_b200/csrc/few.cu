@@ -56,7 +56,7 @@ struct Mxfp4 {};
 template <typename W>
 struct Cfg {
   using XT = W;
-  static constexpr bool MX = false;
+  static constexpr bool MX = false, SPLIT = true;
   static constexpr int STAGES = 4, WK = 4, RED = 2, GATE_UNITS = 4, PASS = 32, EB = sizeof(W);
   static __host__ __device__ constexpr int seg(int nt) { return (nt == 4 ? 256 : 512) / EB; }
   static __host__ __device__ constexpr int wbytes(int c) { return EB * c; }
@@ -64,7 +64,7 @@ struct Cfg {
 template <>
 struct Cfg<Mxfp4> {
   using XT = __nv_bfloat16;
-  static constexpr bool MX = true;
+  static constexpr bool MX = true, SPLIT = false;
   static constexpr int STAGES = 3, WK = 16, RED = 1, GATE_UNITS = 4, PASS = 32, EB = 2;
   static __host__ __device__ constexpr int seg(int nt) { return nt == 1 ? 1024 : 512; }
   static __host__ __device__ constexpr int wbytes(int c) { return c / 2; }
@@ -78,6 +78,10 @@ template <class C> __host__ __device__ constexpr int stage_use(int nt) {
 template <class C> __host__ __device__ constexpr int stage_bytes() {
   int n = stage_use<C>(1) > stage_use<C>(2) ? stage_use<C>(1) : stage_use<C>(2);
   n = n > stage_use<C>(4) ? n : stage_use<C>(4);
+  if (C::SPLIT) {                               // two ranges of 16 rows
+    const int m = 32 * wstride<C>(1) + 8 * (2 * C::EB * C::seg(1) + 64);
+    n = n > m ? n : m;
+  }
   return (n + 511) / 512 * 512;
 }
 constexpr int RED_LD = SLOTS + 4;               // partial sums [token][row], padded: 32 banks
@@ -101,20 +105,52 @@ __device__ __forceinline__ int slot_row(const Tile& t, int s) {
 }
 
 // Weights of the stage at column k0, by one thread: one box per group of 8 rows.  Columns
-// past K arrive as zeros and count as bytes.
+// past K arrive as zeros and count as bytes.  The thread's own steps bound narrow stages, so a
+// full tile's copies are straight-line code.
+template <class C>
+__device__ __forceinline__ void load_box(const CUtensorMap* m, uint8_t* dst, uint64_t* bar, int k0, int row) {
+  if (C::MX) tma_load_3d(m, dst, bar, 0, row, k0 >> 7);
+  else tma_load_2d(m, dst, bar, k0, row);
+}
 template <class C, bool DOWN>
 __device__ __forceinline__ void issue_w(const CUtensorMap* ma, const CUtensorMap* mb, const Tile& t, int k0, int box,
                                         uint8_t* dst, uint64_t* bar) {
-  mbar_arrive_expect_tx(bar, (DOWN ? 1 : 2) * t.nu * box);
-  int row = t.erow + t.base;
-  for (int i = 0; i < t.nu; ++i, row += 8) {
-    if (C::MX) tma_load_3d(ma, dst, bar, 0, row, k0 >> 7);
-    else tma_load_2d(ma, dst, bar, k0, row);
-    dst += box;
-    if (DOWN) continue;
-    if (C::MX) tma_load_3d(mb, dst, bar, 0, row, k0 >> 7);
-    else tma_load_2d(mb, dst, bar, k0, row);
-    dst += box;
+  const int row = t.erow + t.base;
+  if (DOWN) {
+    mbar_arrive_expect_tx(bar, t.sub * t.nu * box);
+    if (C::SPLIT && t.sub == 2) {                // one or two boxes, two column ranges
+      load_box<C>(ma, dst, bar, k0, row);
+      load_box<C>(ma, dst + t.nu * box, bar, k0 + C::seg(1), row);
+      if (t.nu == 2) {
+        load_box<C>(ma, dst + box, bar, k0, row + 8);
+        load_box<C>(ma, dst + 3 * box, bar, k0 + C::seg(1), row + 8);
+      }
+      return;
+    }
+    if (t.nu >= 4) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) load_box<C>(ma, dst + i * box, bar, k0, row + 8 * i);
+#pragma unroll 1
+      for (int i = 4; i < t.nu; ++i) load_box<C>(ma, dst + i * box, bar, k0, row + 8 * i);
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < t.nu; ++i) load_box<C>(ma, dst + i * box, bar, k0, row + 8 * i);
+    }
+  } else {
+    mbar_arrive_expect_tx(bar, 2 * t.nu * box);
+    if (t.nu == 4) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        load_box<C>(ma, dst + 2 * i * box, bar, k0, row + 8 * i);
+        load_box<C>(mb, dst + (2 * i + 1) * box, bar, k0, row + 8 * i);
+      }
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < t.nu; ++i) {
+        load_box<C>(ma, dst + 2 * i * box, bar, k0, row + 8 * i);
+        load_box<C>(mb, dst + (2 * i + 1) * box, bar, k0, row + 8 * i);
+      }
+    }
   }
 }
 __device__ __forceinline__ void cp_async4(uint32_t smem_dst, const void* gsrc) {
@@ -154,7 +190,8 @@ struct Gather {
   }
   __device__ __forceinline__ void tile(const Args& a, const Tables& tb, const Tile& t, int xw, int lane) {
     xs_ld = C::EB * t.seg + 64;
-    xs = SLOTS * C::wbytes(t.seg);
+    // after the weights: 64 rows, or two ranges of 16
+    xs = t.sub == 2 ? 32 * C::wbytes(t.seg / 2) : SLOTS * C::wbytes(t.seg);
 #pragma unroll
     for (int m = 0; m < NTOK; ++m) {
       const int c = xw + X_WARPS * m;            // the stage's token row
@@ -272,9 +309,18 @@ struct Product {
   __device__ __forceinline__ void stage(const Tile& t, int k0, const uint8_t* st, int warp, int lane) {
     constexpr int SEG = C::seg(NT), WS = wstride<C>(NT), XS = xstride<C>(NT);
     const int q = warp & 3, kq = warp >> 2, g = lane >> 2, tq = lane & 3;
-    if ((DOWN ? 2 : 1) * q >= t.nu) return;
-    const int cols = t.K - k0;
-    const uint8_t *wa = st + (16 * q + g) * WS, *xa = st + SLOTS * WS + g * XS;
+    int cols = t.K - k0, xs = XS;
+    const uint8_t *wa = st + (16 * q + g) * WS, *xa = st + SLOTS * WS;
+    if (DOWN && NT == 1 && t.sub == 2) {         // tile row 0 for all: q takes a column range
+      if (q > 1) return;
+      cols -= q * SEG;
+      wa = st + (8 * t.nu * q + g) * WS;
+      xs = 2 * C::EB * SEG + 64;
+      xa = st + 32 * WS + q * C::EB * SEG;
+    } else if ((DOWN ? 2 : 1) * q >= t.nu) {
+      return;
+    }
+    xa += g * xs;
 #pragma unroll
     for (int kk = 0; kk < SEG / 4; kk += 32) {
       const int c = kq * (SEG / 4) + kk + 8 * tq;
@@ -283,7 +329,7 @@ struct Product {
       const uint4 a0 = ok ? lds16(wa + 2 * c) : z, a1 = ok ? lds16(wa + 8 * WS + 2 * c) : z;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const uint4 b = ok && on[n] ? lds16(xa + n * 8 * XS + 2 * c) : z;
+        const uint4 b = ok && on[n] ? lds16(xa + n * 8 * xs + 2 * c) : z;
         mma_bf16(acc[n], a0.x, a1.x, a0.y, a1.y, b.x, b.y);
         mma_bf16(acc[n], a0.z, a1.z, a0.w, a1.w, b.z, b.w);
       }
@@ -318,9 +364,17 @@ struct Product<float, DOWN, NT> {
   __device__ __forceinline__ void stage(const Tile& t, int k0, const uint8_t* st, int warp, int lane) {
     constexpr int SEG = C::seg(NT), WS = wstride<C>(NT), XS = xstride<C>(NT);
     const int q = warp & 3, kq = warp >> 2, g = lane >> 2, tq = lane & 3;
-    if ((DOWN ? 2 : 1) * q >= t.nu) return;
-    const int cols = t.K - k0;
+    int cols = t.K - k0, xs = XS;
     const uint8_t *wa = st + (16 * q + g) * WS, *xa = st + SLOTS * WS;
+    if (DOWN && NT == 1 && t.sub == 2) {         // tile row 0 for all: q takes a column range
+      if (q > 1) return;
+      cols -= q * SEG;
+      wa = st + (8 * t.nu * q + g) * WS;
+      xs = 2 * C::EB * SEG + 64;
+      xa = st + 32 * WS + q * C::EB * SEG;
+    } else if ((DOWN ? 2 : 1) * q >= t.nu) {
+      return;
+    }
 #pragma unroll 1
     for (int kk = 0; kk < SEG / 4; kk += 16) {
       const int c = kq * (SEG / 4) + kk + 4 * tq;
@@ -334,7 +388,7 @@ struct Product<float, DOWN, NT> {
         for (int j = 0; j < 8; ++j) {
           if (!((on >> (8 * n + j)) & 1u)) continue;
           float x[4];
-          unpack16(lds16(xa + (8 * n + j) * XS + 4 * c), x, 0.f);
+          unpack16(lds16(xa + (8 * n + j) * xs + 4 * c), x, 0.f);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             acc[0][n][j] = fmaf(w0[i], x[i], acc[0][n][j]);
@@ -457,7 +511,7 @@ __device__ __forceinline__ void run_pass(const Args& a, Tables& tb, const Tile& 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   Product<W, DOWN, NT> p;
   p.init(t, tb, lane, t.n < 32 ? (1u << t.n) - 1u : 0xffffffffu);
-  for (int k0 = 0; k0 < t.K; k0 += C::seg(NT)) {
+  for (int k0 = 0; k0 < t.K; k0 += t.seg) {
     wait(&tb.full[r.stage], r.phase, tb);
     p.stage(t, k0, stages + r.stage * stage_bytes<C>(), warp, lane);
     __syncwarp();
@@ -487,6 +541,9 @@ __device__ __forceinline__ void run_pass(const Args& a, Tables& tb, const Tile& 
         float v = 0.f;
 #pragma unroll
         for (int w = 0; w < C::WK; ++w) v += rb[(w * 8 + (tid >> 6)) * RED_LD + s];
+        if (t.sub == 2)
+#pragma unroll
+          for (int w = 0; w < C::WK; ++w) v += rb[(w * 8 + (tid >> 6)) * RED_LD + s + 16];
         if (C::MX) v *= inverse_pow2(token_scale<DOWN>(t, tb, i));
         const int tok = t.sh ? t.row + i : tb.row_tok[t.row + i];
         yacc[tok * SLOTS + s] += v * (t.sh ? tb.shw[tok] : tb.row_w[t.row + i]);
@@ -560,7 +617,7 @@ __device__ __forceinline__ void run_down_by_token(const Args& a, Tables& tb, Wal
     }
     p.init(t, tb, lane, cols);
     if constexpr (C::MX) p.scale_of(t, tb, mine);
-    for (int k0 = 0; k0 < t.K; k0 += C::seg(1)) {
+    for (int k0 = 0; k0 < t.K; k0 += t.seg) {
       wait(&tb.full[r.stage], r.phase, tb);
       p.stage(t, k0, stages + r.stage * stage_bytes<C>(), warp, lane);
       __syncwarp();
@@ -586,6 +643,9 @@ __device__ __forceinline__ void run_down_by_token(const Args& a, Tables& tb, Wal
       float v = 0.f;
 #pragma unroll
       for (int k = 0; k < C::WK; ++k) v += red[(k * 8 + tok) * RED_LD + (tid & 63)];
+      if (t.sub == 2)
+#pragma unroll
+        for (int k = 0; k < C::WK; ++k) v += red[(k * 8 + tok) * RED_LD + (tid & 63) + 16];
       y[(size_t)tok * a.d + j] = (XT)v;
     }
     worker_sync();
@@ -626,7 +686,7 @@ few_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps) {
     auto stream = [&](auto walk) {
       Tile t;
       while (walk.next(t)) {
-        const int v = t.seg != C::seg(1), box = 8 * C::wbytes(t.seg);
+        const int seg = t.seg / t.sub, v = seg != C::seg(1), box = 8 * C::wbytes(seg);
         for (int k0 = 0; k0 < t.K && !tb.abort; k0 += t.seg) {
           wait(&tb.empty[r.stage], r.phase ^ 1u, tb);
           if (lane == 0)
@@ -679,7 +739,7 @@ few_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps) {
     Ring r{0, 0};
     int buf = 0;
     Tile t;
-    router_logits<XT>(a, reinterpret_cast<float4*>(red));
+    router_logits<XT>(a, red);
     worker_sync();
     if (tid == 0) grid_arrive(a.bar + BAR_LOGITS);
     if (C::MX) {                           // each token's largest x, for fp16

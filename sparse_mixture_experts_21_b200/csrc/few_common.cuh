@@ -117,7 +117,12 @@ __device__ __forceinline__ void worker_sync() { asm volatile("bar.sync 1, %0;" :
 __host__ __device__ __forceinline__ int route_tiles(int ld) { return (ld + ROUTE_TILE - 1) / ROUTE_TILE; }
 // One job for every SM of the grid (144 in all), slices of at least 256 columns and 16 at most
 // (the selection adds them one by one), but none wider than the registers hold.
-__host__ __device__ __forceinline__ int route_slices(int ld, int d) {
+// With up to WHOLE_T tokens x is little to read and every CTA takes two experts' whole rows:
+// no partial sums (their adding up would be the selection's longest step: 13 us of one warp
+// for 256 experts in 9 slices, under the shared experts' stream).
+constexpr int WHOLE_T = 4;
+__host__ __device__ __forceinline__ int route_slices(int ld, int d, int T) {
+  if (T <= WHOLE_T) return 1;
   int n = 144 / route_tiles(ld);
   const int most = (d + 255) / 256, least = (d + ROUTE_COLS - 1) / ROUTE_COLS;
   n = n < most ? n : most;
@@ -140,12 +145,58 @@ __device__ __forceinline__ float4 quad_f32(const uint2& v) {
 template <typename XT> struct Quad { using T = uint2; };
 template <> struct Quad<float> { using T = uint4; };
 
-// By the CTA's first 16 warps; xs: 32 KB of shared memory.
+// Whole rows: warps 0, 2, .. take expert blockIdx.x (+ 2 grid ..), the others the one a grid
+// further, an eighth of the columns each; part: 64 floats of shared memory.
 template <typename XT>
-__device__ __forceinline__ void router_logits(const Args& a, float4* xs) {
+__device__ __forceinline__ void router_logits_whole(const Args& a, float* part) {
+  constexpr int SL = WORKERS / 2;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, P = gridDim.x;
+  const int ld = a.N + a.sink, quads = a.d / 4;
+  const XT* x = static_cast<const XT*>(a.x);
+  for (int e0 = blockIdx.x; e0 < ld; e0 += 2 * P) {
+    const int e = e0 + (warp & 1) * P;
+    const float4* wg = reinterpret_cast<const float4*>(a.w_gate + (size_t)min(e, ld - 1) * a.d);
+    float acc[WHOLE_T] = {};
+#pragma unroll 4
+    for (int q = (warp >> 1) * 32 + lane; q < quads; q += 32 * SL) {
+      const float4 w = __ldg(wg + q);
+#pragma unroll
+      for (int j = 0; j < WHOLE_T; ++j) {
+        if (j >= a.T) break;
+        typename Quad<XT>::T v;
+        ldg_quad(x + (size_t)j * a.d + 4 * q, v);
+        const float4 b = quad_f32(v);
+        acc[j] = fmaf(w.x, b.x, fmaf(w.y, b.y, fmaf(w.z, b.z, fmaf(w.w, b.w, acc[j]))));
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < WHOLE_T; ++j) {
+      acc[j] = warp_sum(acc[j]);
+      if (lane == 0) part[warp * WHOLE_T + j] = acc[j];
+    }
+    worker_sync();
+    if (tid < 2 * WHOLE_T) {
+      const int j = tid >> 1, i = tid & 1;
+      float v = 0.f;
+#pragma unroll
+      for (int s = 0; s < SL; ++s) v += part[(2 * s + i) * WHOLE_T + j];
+      if (j < a.T && e0 + i * P < ld) a.logits[(size_t)j * route_ld(ld) + e0 + i * P] = v;
+    }
+    worker_sync();
+  }
+}
+
+// By the CTA's first 16 warps; part: 32 KB of shared memory.
+template <typename XT>
+__device__ __forceinline__ void router_logits(const Args& a, float* part) {
+  if (a.T <= WHOLE_T) {
+    router_logits_whole<XT>(a, part);
+    return;
+  }
+  float4* xs = reinterpret_cast<float4*>(part);
   constexpr int QUADS = ROUTE_COLS / 4, PER = 8 * QUADS / (32 * WORKERS);   // a thread's share of eight tokens
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int ld = a.N + a.sink, tiles = route_tiles(ld), slices = route_slices(ld, a.d);
+  const int ld = a.N + a.sink, tiles = route_tiles(ld), slices = route_slices(ld, a.d, a.T);
   const int quads = (a.d / 4 + slices - 1) / slices;
   const XT* x = static_cast<const XT*>(a.x);
   for (int job = blockIdx.x; job < tiles * slices; job += gridDim.x) {
@@ -213,7 +264,7 @@ __device__ __noinline__ void select_token(const Args& a, Tables& tb, int t) {
   float* sv = sc.sv;
   uint32_t* q = sc.q;
   const int lane = threadIdx.x & 31, N = a.N, k = a.k;
-  const int ld = N + a.sink, slices = route_slices(ld, a.d);
+  const int ld = N + a.sink, slices = route_slices(ld, a.d, a.T);
   const rt::RouteArgs& r = a.route;
   // the slices' sums, through shared memory: one wait for as many as fit
   const int ldp = route_ld(ld), per = PART / ldp;
@@ -447,12 +498,12 @@ struct Tile {
   int nu;             // units
   int n;              // tokens of this pass
   int row;            // first hidden row (routed: table row; shared: token), this pass
-  int nt, seg;
+  int nt, sub, seg;   // 8-token columns; column ranges of a stage, columns of a stage
   bool sh, last;      // last: the tile's last pass (down: of the last expert)
 };
 
 // C::seg(nt): columns of a stage; C::GATE_UNITS: units of a gate/up tile; C::PASS: tokens of an
-// expert per pass over its weights.
+// expert per pass over its weights; C::SPLIT: two column ranges a stage for narrow down tiles.
 template <class C, bool DOWN>
 struct Walk {
   static constexpr bool kDown = DOWN;
@@ -502,7 +553,10 @@ struct Walk {
     t.n = min(n - done, C::PASS);
     t.row = (shared ? 0 : tb->row0[e]) + done;
     t.nt = t.n <= 8 ? 1 : t.n <= 16 ? 2 : 4;
-    t.seg = C::seg(t.nt);
+    // a narrow down tile takes two column ranges a stage, for warps and bytes in flight that a
+    // wide one gets from its rows
+    t.sub = DOWN && C::SPLIT && t.nt == 1 && t.nu <= 2 ? 2 : 1;
+    t.seg = C::seg(t.nt) * t.sub;
     done += t.n;
     t.last = false;
     if (done < n) return true;
@@ -533,7 +587,7 @@ size_t zero_bytes(const moe_config_t& c) { return align256(256 + (size_t)c.T * (
 size_t shw_bytes(const moe_config_t& c) { return align256((size_t)c.T * 4); }
 size_t logit_bytes(const moe_config_t& c) {
   const int ld = c.n_experts + c.shared_sink;
-  return align256((size_t)route_slices(ld, c.d_model) * c.T * route_ld(ld) * 4);
+  return align256((size_t)route_slices(ld, c.d_model, (int)c.T) * c.T * route_ld(ld) * 4);
 }
 
 }  // namespace few
