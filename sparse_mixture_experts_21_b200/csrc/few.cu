@@ -17,9 +17,9 @@
 //   down       each CTA takes rows of W2 of all met experts, so a token's sum over its
 //              experts stays inside one CTA: fixed order, no atomics, no second pass
 //
-// One warp streams the weights through a ring of shared-memory stages with TMA, 8 rows by 512
-// bytes a copy (4 KB: at 512 bytes a copy, the engine's ~57 cycles for one would hold the
-// stream to 2.5 TB/s), and runs ahead of the phases: the first down stages' weights are in
+// One warp streams the weights through a ring of shared-memory stages with TMA, 8 or 32 rows by
+// 512 bytes a copy (at 512 bytes a copy, the engine's ~57 cycles for one would hold the stream
+// to 2.5 TB/s), and runs ahead of the phases: the first down stages' weights are in
 // flight while the CTA waits at barrier 2 for the hidden rows.  Two warps gather the same
 // columns of the expert's tokens with cp.async.  Sixteen warps multiply with mma.sync
 // m16n8k16: 16 weight rows by 8 tokens, which leaves nothing to gain from tcgen05 (its
@@ -42,12 +42,12 @@ constexpr int W_WARP = WARPS, X_WARP0 = WARPS + 1, SELECT_WARP = X_WARP0 + X_WAR
 constexpr int CONSUMERS = 32 * WARPS, THREADS = 32 * (SELECT_WARP + 1);
 
 struct Maps {
-  CUtensorMap m[6][2];     // boxes of 8 rows by a stage's columns: for 16 tokens, for 32
+  CUtensorMap m[6][2][2];  // boxes of a stage's columns (for 16 tokens, for 32) by 8 and by 32 rows
 };
 
 // Per weight type W (fp32 and bf16: x and weights; Mxfp4: bf16 x).  nt: 8-token columns of a
-// pass (1, 2 or 4); seg(nt): columns of a stage.  A stage holds 8 groups of 8 weight rows as
-// TMA leaves them (fp32, bf16: row by row; MXFP4: by 64-byte column chunks, the chunk's 8 rows,
+// pass (1, 2 or 4); seg(nt): columns of a stage.  A stage holds up to 64 weight rows as TMA
+// leaves them (fp32, bf16: row by row, 32 gate rows before 32 up rows; MXFP4, in groups of 8: by 64-byte column chunks, the chunk's 8 rows,
 // 64-byte swizzle, so that the 16 bytes that a quad takes of each of 8 rows fall into
 // different banks), then the tokens' rows, 64 mod 128 bytes apart so that a quarter warp's
 // 16-byte reads meet every bank once, then MXFP4's scales, 36 bytes a row.
@@ -104,9 +104,10 @@ __device__ __forceinline__ int slot_row(const Tile& t, int s) {
   return r < 8 * t.nu ? t.base + r : -1;
 }
 
-// Weights of the stage at column k0, by one thread: one box per group of 8 rows.  Columns
-// past K arrive as zeros and count as bytes.  The thread's own steps bound narrow stages, so a
-// full tile's copies are straight-line code.
+// Weights of the stage at column k0, by one thread, in boxes of 32 rows and of 8 (MXFP4: 8);
+// m[0], m[1]: the 8-row and the 32-row map.  Columns past K arrive as zeros and count as bytes.
+// The thread's own steps would bound the stream (eight 8-row copies a stage took 5% longer
+// than two 32-row ones), so there are few and none in loops where the tile is full.
 template <class C>
 __device__ __forceinline__ void load_box(const CUtensorMap* m, uint8_t* dst, uint64_t* bar, int k0, int row) {
   if (C::MX) tma_load_3d(m, dst, bar, 0, row, k0 >> 7);
@@ -127,18 +128,24 @@ __device__ __forceinline__ void issue_w(const CUtensorMap* ma, const CUtensorMap
       }
       return;
     }
-    if (t.nu >= 4) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) load_box<C>(ma, dst + i * box, bar, k0, row + 8 * i);
-#pragma unroll 1
-      for (int i = 4; i < t.nu; ++i) load_box<C>(ma, dst + i * box, bar, k0, row + 8 * i);
-    } else {
-#pragma unroll 1
-      for (int i = 0; i < t.nu; ++i) load_box<C>(ma, dst + i * box, bar, k0, row + 8 * i);
+    int i = 0;
+    if (!C::MX && t.nu >= 4) {
+      load_box<C>(ma + 1, dst, bar, k0, row);
+      i = 4;
+      if (t.nu == 8) {
+        load_box<C>(ma + 1, dst + 4 * box, bar, k0, row + 32);
+        i = 8;
+      }
     }
+#pragma unroll 1
+    for (; i < t.nu; ++i) load_box<C>(ma, dst + i * box, bar, k0, row + 8 * i);
   } else {
     mbar_arrive_expect_tx(bar, 2 * t.nu * box);
-    if (t.nu == 4) {
+    // gate and up rows: MXFP4 8 and 8 in turn, else 32 after 32
+    if (!C::MX && t.nu == 4) {
+      load_box<C>(ma + 1, dst, bar, k0, row);
+      load_box<C>(mb + 1, dst + 4 * box, bar, k0, row);
+    } else if (C::MX && t.nu == 4) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         load_box<C>(ma, dst + 2 * i * box, bar, k0, row + 8 * i);
@@ -147,8 +154,8 @@ __device__ __forceinline__ void issue_w(const CUtensorMap* ma, const CUtensorMap
     } else {
 #pragma unroll 1
       for (int i = 0; i < t.nu; ++i) {
-        load_box<C>(ma, dst + 2 * i * box, bar, k0, row + 8 * i);
-        load_box<C>(mb, dst + (2 * i + 1) * box, bar, k0, row + 8 * i);
+        load_box<C>(ma, dst + (C::MX ? 2 * i : i) * box, bar, k0, row + 8 * i);
+        load_box<C>(mb, dst + (C::MX ? 2 * i + 1 : i + 4) * box, bar, k0, row + 8 * i);
       }
     }
   }
@@ -310,7 +317,8 @@ struct Product {
     constexpr int SEG = C::seg(NT), WS = wstride<C>(NT), XS = xstride<C>(NT);
     const int q = warp & 3, kq = warp >> 2, g = lane >> 2, tq = lane & 3;
     int cols = t.K - k0, xs = XS;
-    const uint8_t *wa = st + (16 * q + g) * WS, *xa = st + SLOTS * WS;
+    constexpr int UP = (DOWN ? 8 : 32) * WS;      // to the row of the tile's lower half
+    const uint8_t *wa = st + ((DOWN ? 16 : 8) * q + g) * WS, *xa = st + SLOTS * WS;
     if (DOWN && NT == 1 && t.sub == 2) {         // tile row 0 for all: q takes a column range
       if (q > 1) return;
       cols -= q * SEG;
@@ -326,7 +334,7 @@ struct Product {
       const int c = kq * (SEG / 4) + kk + 8 * tq;
       const uint4 z = make_uint4(0, 0, 0, 0);
       const bool ok = c < cols;
-      const uint4 a0 = ok ? lds16(wa + 2 * c) : z, a1 = ok ? lds16(wa + 8 * WS + 2 * c) : z;
+      const uint4 a0 = ok ? lds16(wa + 2 * c) : z, a1 = ok ? lds16(wa + UP + 2 * c) : z;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const uint4 b = ok && on[n] ? lds16(xa + n * 8 * xs + 2 * c) : z;
@@ -365,7 +373,8 @@ struct Product<float, DOWN, NT> {
     constexpr int SEG = C::seg(NT), WS = wstride<C>(NT), XS = xstride<C>(NT);
     const int q = warp & 3, kq = warp >> 2, g = lane >> 2, tq = lane & 3;
     int cols = t.K - k0, xs = XS;
-    const uint8_t *wa = st + (16 * q + g) * WS, *xa = st + SLOTS * WS;
+    constexpr int UP = (DOWN ? 8 : 32) * WS;      // to the row of the tile's lower half
+    const uint8_t *wa = st + ((DOWN ? 16 : 8) * q + g) * WS, *xa = st + SLOTS * WS;
     if (DOWN && NT == 1 && t.sub == 2) {         // tile row 0 for all: q takes a column range
       if (q > 1) return;
       cols -= q * SEG;
@@ -381,7 +390,7 @@ struct Product<float, DOWN, NT> {
       if (c >= cols) continue;
       float w0[4], w1[4];
       unpack16(lds16(wa + 4 * c), w0, 0.f);
-      unpack16(lds16(wa + 8 * WS + 4 * c), w1, 0.f);
+      unpack16(lds16(wa + UP + 4 * c), w1, 0.f);
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -690,7 +699,7 @@ few_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps) {
         for (int k0 = 0; k0 < t.K && !tb.abort; k0 += t.seg) {
           wait(&tb.empty[r.stage], r.phase ^ 1u, tb);
           if (lane == 0)
-            issue_w<C, decltype(walk)::kDown>(&maps.m[t.ma][v], &maps.m[t.mb][v], t, k0, box,
+            issue_w<C, decltype(walk)::kDown>(maps.m[t.ma][v], maps.m[t.mb][v], t, k0, box,
                                               smem + r.stage * stage_bytes<C>(), &tb.full[r.stage]);
           __syncwarp();
           ++issued;
@@ -809,8 +818,9 @@ cudaError_t launch(const Args& a, const void* const* w, size_t zero, cudaStream_
     const uint64_t all = (uint64_t)(shared ? 1 : a.N) * rows;
     // the narrow boxes serve passes of 17 tokens and more (MXFP4: of 9)
     for (int v = 0; v < (a.T > (C::MX ? 8 : 16) ? 2 : 1); ++v)
-      if (!(C::MX ? make_map_u4_rows8(&maps.m[i][v], w[i], all, cols, C::seg(v ? 4 : 1) / 128)
-                  : make_map_rows8(&maps.m[i][v], w[i], C::EB == 4, all, cols, C::seg(v ? 4 : 1))))
+      if (C::MX ? !make_map_u4_rows8(&maps.m[i][v][0], w[i], all, cols, C::seg(v ? 4 : 1) / 128)
+                : !make_map_rows(&maps.m[i][v][0], w[i], C::EB == 4, all, cols, C::seg(v ? 4 : 1), 8) ||
+                      !make_map_rows(&maps.m[i][v][1], w[i], C::EB == 4, all, cols, C::seg(v ? 4 : 1), 32))
         return cudaErrorInvalidValue;
   }
   const void* fn = (const void*)few_kernel<W>;

@@ -15,7 +15,8 @@ namespace moe {
 bool make_map_bf16(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows);
 bool make_map_u8(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows);
 bool make_map_u4(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows);
-bool make_map_rows8(CUtensorMap* m, const void* base, bool f32, uint64_t rows, uint64_t cols, uint32_t box_cols);
+bool make_map_rows(CUtensorMap* m, const void* base, bool f32, uint64_t rows, uint64_t cols, uint32_t box_cols,
+                   uint32_t box_rows);
 bool make_map_u4_rows8(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t chunks);
 bool make_map_bf16_store32(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols);
 
