@@ -455,7 +455,7 @@ int moe_grouped_ffn_mxfp8(const moe_config_t* cfg, const uint8_t* xq_rows, const
  *   q        [rows, cols / 2] uint8 out; sf E8M0 scales out, plain-matrix tile atoms
  * Expert weights [G, f, d] are quantised as rows = G * f (blocks never span rows).
  * Errors: MOE_ERR_INVALID_ARG for a bad shape or type or a NULL or misaligned
- * (16-byte) pointer; MOE_ERR_UNSUPPORTED past 2^43 elements.  rows = 0 is a no-op. */
+ * (16-byte) pointer; MOE_ERR_UNSUPPORTED past 2^39 elements.  rows = 0 is a no-op. */
 int moe_quantize_mxfp4(const void* x, int32_t x_dtype, int64_t rows, int32_t cols, uint8_t* q, uint8_t* sf,
                        void* stream);
 

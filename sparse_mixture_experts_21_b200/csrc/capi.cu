@@ -447,7 +447,7 @@ int moe_quantize_mxfp4(const void* x, int32_t x_dtype, int64_t rows, int32_t col
   if (rows < 0 || cols <= 0 || (cols % 128) != 0) return MOE_ERR_INVALID_ARG;
   if (x_dtype != MOE_DTYPE_F32 && x_dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARG;
   if (rows == 0) return MOE_OK;
-  if (rows > ((int64_t)1 << 43) / cols) return MOE_ERR_UNSUPPORTED;
+  if (rows > ((int64_t)1 << 39) / cols) return MOE_ERR_UNSUPPORTED;
   if (!x || !q || !sf || !aligned16(x) || !aligned16(q) || !aligned16(sf)) return MOE_ERR_INVALID_ARG;
   return from_cuda(launch_mx4_quant(x, x_dtype == MOE_DTYPE_F32, rows, cols, q, sf, static_cast<cudaStream_t>(stream)));
 }
@@ -457,7 +457,7 @@ int moe_dequantize_mxfp4(const uint8_t* q, const uint8_t* sf, int64_t rows, int3
   if (rows < 0 || cols <= 0 || (cols % 128) != 0) return MOE_ERR_INVALID_ARG;
   if (y_dtype != MOE_DTYPE_F32 && y_dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARG;
   if (rows == 0) return MOE_OK;
-  if (rows > ((int64_t)1 << 43) / cols) return MOE_ERR_UNSUPPORTED;
+  if (rows > ((int64_t)1 << 39) / cols) return MOE_ERR_UNSUPPORTED;
   if (!q || !sf || !y || !aligned16(q) || !aligned16(sf) || !aligned16(y)) return MOE_ERR_INVALID_ARG;
   return from_cuda(launch_mx4_dequant(q, sf, rows, cols, y_dtype == MOE_DTYPE_F32, y, static_cast<cudaStream_t>(stream)));
 }

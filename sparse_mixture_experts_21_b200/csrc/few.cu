@@ -259,16 +259,6 @@ __device__ __forceinline__ void mma_f16(float* d, uint32_t a0, uint32_t a1, uint
                : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
-// Eight E2M1 codes of a word to four pairs of fp16 (exact), in order.
-__device__ __forceinline__ void e2m1_f16(uint32_t w, uint32_t* o) {
-  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-      : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]) : "r"(w));
-}
 // Two bf16 to fp16, times a power of two.
 __device__ __forceinline__ uint32_t scaled_f16(uint32_t v, float s) {
   const __half2 h = __floats2half2_rn(__uint_as_float(v << 16) * s, __uint_as_float(v & 0xffff0000u) * s);
@@ -484,8 +474,8 @@ struct Product<Mxfp4, DOWN, NT> {
 #pragma unroll
       for (int k = 0; k < BLOCKS; ++k) {
         uint32_t a0[4], a1[4];
-        e2m1_f16(lds4(wu[k] + 16 * q * WS), a0);
-        e2m1_f16(lds4(wu[k] + (16 * q + 8) * WS), a1);
+        mx4::e2m1_f16(lds4(wu[k] + 16 * q * WS), a0);
+        mx4::e2m1_f16(lds4(wu[k] + (16 * q + 8) * WS), a1);
         // 2^(byte - 127) as a float: byte 0 stands for 2^-127 and counts as 0 (such a block's
         // products are below fp32's normal range); 255 (NaN) becomes an infinity, which times
         // the zero codes of such a block is NaN
