@@ -109,53 +109,54 @@ __device__ __forceinline__ int slot_row(const Tile& t, int s) {
 // The thread's own steps would bound the stream (eight 8-row copies a stage took 5% longer
 // than two 32-row ones), so there are few and none in loops where the tile is full.
 template <class C>
-__device__ __forceinline__ void load_box(const CUtensorMap* m, uint8_t* dst, uint64_t* bar, int k0, int row) {
-  if (C::MX) tma_load_3d(m, dst, bar, 0, row, k0 >> 7);
-  else tma_load_2d(m, dst, bar, k0, row);
+__device__ __forceinline__ void load_box(const CUtensorMap* m, uint8_t* dst, uint64_t* bar, int k0, int row,
+                                         uint64_t policy) {
+  if (C::MX) tma_load_3d(m, dst, bar, 0, row, k0 >> 7, policy);
+  else tma_load_2d(m, dst, bar, k0, row, policy);
 }
 template <class C, bool DOWN>
 __device__ __forceinline__ void issue_w(const CUtensorMap* ma, const CUtensorMap* mb, const Tile& t, int k0, int box,
-                                        uint8_t* dst, uint64_t* bar) {
+                                        uint8_t* dst, uint64_t* bar, uint64_t policy) {
   const int row = t.erow + t.base;
   if (DOWN) {
     mbar_arrive_expect_tx(bar, t.sub * t.nu * box);
     if (C::SPLIT && t.sub == 2) {                // one or two boxes, two column ranges
-      load_box<C>(ma, dst, bar, k0, row);
-      load_box<C>(ma, dst + t.nu * box, bar, k0 + C::seg(1), row);
+      load_box<C>(ma, dst, bar, k0, row, policy);
+      load_box<C>(ma, dst + t.nu * box, bar, k0 + C::seg(1), row, policy);
       if (t.nu == 2) {
-        load_box<C>(ma, dst + box, bar, k0, row + 8);
-        load_box<C>(ma, dst + 3 * box, bar, k0 + C::seg(1), row + 8);
+        load_box<C>(ma, dst + box, bar, k0, row + 8, policy);
+        load_box<C>(ma, dst + 3 * box, bar, k0 + C::seg(1), row + 8, policy);
       }
       return;
     }
     int i = 0;
     if (!C::MX && t.nu >= 4) {
-      load_box<C>(ma + 1, dst, bar, k0, row);
+      load_box<C>(ma + 1, dst, bar, k0, row, policy);
       i = 4;
       if (t.nu == 8) {
-        load_box<C>(ma + 1, dst + 4 * box, bar, k0, row + 32);
+        load_box<C>(ma + 1, dst + 4 * box, bar, k0, row + 32, policy);
         i = 8;
       }
     }
 #pragma unroll 1
-    for (; i < t.nu; ++i) load_box<C>(ma, dst + i * box, bar, k0, row + 8 * i);
+    for (; i < t.nu; ++i) load_box<C>(ma, dst + i * box, bar, k0, row + 8 * i, policy);
   } else {
     mbar_arrive_expect_tx(bar, 2 * t.nu * box);
     // gate and up rows: MXFP4 8 and 8 in turn, else 32 after 32
     if (!C::MX && t.nu == 4) {
-      load_box<C>(ma + 1, dst, bar, k0, row);
-      load_box<C>(mb + 1, dst + 4 * box, bar, k0, row);
+      load_box<C>(ma + 1, dst, bar, k0, row, policy);
+      load_box<C>(mb + 1, dst + 4 * box, bar, k0, row, policy);
     } else if (C::MX && t.nu == 4) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        load_box<C>(ma, dst + 2 * i * box, bar, k0, row + 8 * i);
-        load_box<C>(mb, dst + (2 * i + 1) * box, bar, k0, row + 8 * i);
+        load_box<C>(ma, dst + 2 * i * box, bar, k0, row + 8 * i, policy);
+        load_box<C>(mb, dst + (2 * i + 1) * box, bar, k0, row + 8 * i, policy);
       }
     } else {
 #pragma unroll 1
       for (int i = 0; i < t.nu; ++i) {
-        load_box<C>(ma, dst + (C::MX ? 2 * i : i) * box, bar, k0, row + 8 * i);
-        load_box<C>(mb, dst + (C::MX ? 2 * i + 1 : i + 4) * box, bar, k0, row + 8 * i);
+        load_box<C>(ma, dst + (C::MX ? 2 * i : i) * box, bar, k0, row + 8 * i, policy);
+        load_box<C>(mb, dst + (C::MX ? 2 * i + 1 : i + 4) * box, bar, k0, row + 8 * i, policy);
       }
     }
   }
@@ -263,6 +264,11 @@ __device__ __forceinline__ void mma_f16(float* d, uint32_t a0, uint32_t a1, uint
 __device__ __forceinline__ uint32_t scaled_f16(uint32_t v, float s) {
   const __half2 h = __floats2half2_rn(__uint_as_float(v << 16) * s, __uint_as_float(v & 0xffff0000u) * s);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Scale bytes of two blocks to 2^(byte - 127) as two bf16: byte 0 to the subnormal 2^-127; 255
+// (NaN) to an infinity, which times the zero codes of such a block is NaN.
+__device__ __forceinline__ uint32_t scale_pair(uint32_t s) {
+  return __vmaxu2(__byte_perm(s, 0, 0x4140) << 7, 0x00400040u);
 }
 // fp16 holds bf16's eight significant bits but not its range: a row goes to fp16 times the
 // power of two that brings its largest value (given as bits) to [2^14, 2^15).  What falls
@@ -417,7 +423,7 @@ struct Product<float, DOWN, NT> {
 // the conversion of 4-bit codes, where HBM would allow 47 at one a clock.  The block-scaled
 // tensor cores take the codes as they are, but not at this shape: an M = 128 x K = 32 MMA
 // costs ~200 cycles however few tokens there are, 800 for the 8.7 KB of codes that HBM
-// brings in 357 (measured with that kernel: 193 us against this one's for one token).
+// brings in 357 (measured with that kernel: 1.93 ms for 24 tokens against this one's 1.06).
 template <bool DOWN, int NT>
 struct Product<Mxfp4, DOWN, NT> {
   using C = Cfg<Mxfp4>;
@@ -469,18 +475,15 @@ struct Product<Mxfp4, DOWN, NT> {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       // scale bytes of this row and the one 8 below, for the warp's one or two blocks
-      const uint32_t s0 = BLOCKS == 2 ? lds2(sa + 16 * SF_LD * q) : lds1(sa + 16 * SF_LD * q);
-      const uint32_t s1 = BLOCKS == 2 ? lds2(sa + (16 * q + 8) * SF_LD) : lds1(sa + (16 * q + 8) * SF_LD);
+      const uint32_t s0 = scale_pair(BLOCKS == 2 ? lds2(sa + 16 * SF_LD * q) : lds1(sa + 16 * SF_LD * q));
+      const uint32_t s1 = scale_pair(BLOCKS == 2 ? lds2(sa + (16 * q + 8) * SF_LD) : lds1(sa + (16 * q + 8) * SF_LD));
 #pragma unroll
       for (int k = 0; k < BLOCKS; ++k) {
         uint32_t a0[4], a1[4];
         mx4::e2m1_f16(lds4(wu[k] + 16 * q * WS), a0);
         mx4::e2m1_f16(lds4(wu[k] + (16 * q + 8) * WS), a1);
-        // 2^(byte - 127) as a float: byte 0 stands for 2^-127 and counts as 0 (such a block's
-        // products are below fp32's normal range); 255 (NaN) becomes an infinity, which times
-        // the zero codes of such a block is NaN
-        const float f0 = __uint_as_float((s0 << (23 - 8 * k)) & 0x7f800000u);
-        const float f1 = __uint_as_float((s1 << (23 - 8 * k)) & 0x7f800000u);
+        const float f0 = __uint_as_float(k ? s0 & 0xffff0000u : s0 << 16);
+        const float f1 = __uint_as_float(k ? s1 & 0xffff0000u : s1 << 16);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           float p[4];
@@ -680,6 +683,9 @@ few_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps) {
 
   if (warp == W_WARP) {
     // ---------------------------------------------------------------- weights
+    // read once: scales, hidden rows and sums stay in L2 beside the stream (MXFP4 with one token
+    // 108 -> 101 us, bf16 149 -> 147)
+    const uint64_t policy = l2_evict_first();
     Ring r{0, 0};
     int issued = 0;
     auto stream = [&](auto walk) {
@@ -690,7 +696,7 @@ few_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps) {
           wait(&tb.empty[r.stage], r.phase ^ 1u, tb);
           if (lane == 0)
             issue_w<C, decltype(walk)::kDown>(maps.m[t.ma][v], maps.m[t.mb][v], t, k0, box,
-                                              smem + r.stage * stage_bytes<C>(), &tb.full[r.stage]);
+                                              smem + r.stage * stage_bytes<C>(), &tb.full[r.stage], policy);
           __syncwarp();
           ++issued;
           r.next(C::STAGES);

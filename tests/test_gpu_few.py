@@ -337,3 +337,45 @@ def test_a_prompt_and_then_its_next_tokens(mode):
         x.copy_(inp["x"][lo:lo + 4])
         g.replay()
         assert torch.equal(out, lay.forward_few(inp["x"][lo:lo + 4].contiguous()))
+
+
+def test_mxfp4_scale_byte_zero_counts():
+    """Blocks of the smallest scale, 2^-127, under tokens large enough that their products are
+    ordinary numbers."""
+    T, N, d, f = 3, 4, 256, 128
+    g = torch.Generator(device="cuda").manual_seed(9)
+    x = (torch.randn(T, d, generator=g, device="cuda") * 2.0 ** 100).bfloat16()
+    w = Workload("zero", T=T, N=N, k=2, d=d, f=f, n_shared=0, f_shared=0)
+    wg = torch.randn(N, d, generator=g, device="cuda") * 2.0 ** -104
+    w1 = torch.randn(N * f, d, generator=g, device="cuda") * 2.0 ** -128
+    w3 = torch.randn(N * f, d, generator=g, device="cuda") * 2.0 ** -128
+    w2 = torch.randn(N * d, f, generator=g, device="cuda") * 2.0 ** 40
+    packs = []
+    for m in (w1, w3, w2):
+        q = torch.empty(m.shape[0], m.shape[1] // 2, dtype=torch.uint8, device="cuda")
+        sf = L.mx_scales(m.shape[0], m.shape[1], "cuda")
+        L.moe_quantize_mxfp4(m.float(), q, sf)
+        packs.append((q, sf))
+    assert int((packs[0][1] == 0).sum()) == N * f * d // 32
+    c = make_config(w)
+    ws = torch.empty(L.few_tokens_workspace_size(c, 0), dtype=torch.uint8, device="cuda")
+    idx = torch.empty(T, 2, dtype=torch.int32, device="cuda")
+    tw = torch.empty(T, 2, device="cuda")
+    y = torch.empty(T, d, dtype=torch.bfloat16, device="cuda")
+    L.moe_few_tokens_mxfp4(c, x, wg, None, None, *packs, None, None, None, 0, idx, tw, y, ws)
+    deq = []
+    for (q, sf), m in zip(packs, (w1, w3, w2)):
+        v = torch.empty_like(m)
+        L.moe_dequantize_mxfp4(q, sf, v)
+        deq.append(v.double().view(N, -1, m.shape[1]))
+    ref = torch.zeros(T, d, dtype=torch.float64, device="cuda")
+    for t in range(T):
+        for j in range(2):
+            e = int(idx[t, j])
+            a, b = deq[0][e] @ x[t].double(), deq[1][e] @ x[t].double()
+            h = (a * torch.sigmoid(a) * b).bfloat16().double()
+            ref[t] += tw[t, j].double() * (deq[2][e] @ h)
+    assert float(ref.abs().max()) > 0
+    # y rounds to bf16 (2^-8 of itself); h may round the other way (2^-7 of one step of h): with
+    # the sums' fp32 error far below, 2^-6 of the row's norm bounds both
+    assert float((y.double() - ref).norm()) <= 2.0 ** -6 * float(ref.norm())
