@@ -259,12 +259,13 @@ __device__ __forceinline__ void next_best(const uint32_t* q, int lo, int hi, int
 
 // Selection for token t by one warp: moe_route's formulas, ties and order, in loops instead of
 // registers (a few tokens meet this code once, cold: its size counts more than its steps).
-__device__ __noinline__ void select_token(const Args& a, Tables& tb, int t) {
+// dry (N = 1, k = 1, t = 0): all of its steps on some word of x, and no results.
+__device__ __noinline__ void select_token(const Args& a, Tables& tb, int t, int N, int k, bool dry) {
   Scratch& sc = tb.sc;
   float* sv = sc.sv;
   uint32_t* q = sc.q;
-  const int lane = threadIdx.x & 31, N = a.N, k = a.k;
-  const int ld = N + a.sink, slices = route_slices(ld, a.d, a.T);
+  const int lane = threadIdx.x & 31;
+  const int ld = N + a.sink, slices = dry ? 1 : route_slices(ld, a.d, a.T);
   const rt::RouteArgs& r = a.route;
   // the slices' sums, through shared memory: one wait for as many as fit
   const int ldp = route_ld(ld), per = PART / ldp;
@@ -273,7 +274,7 @@ __device__ __noinline__ void select_token(const Args& a, Tables& tb, int t) {
     const int n = min(per, slices - s0);
 #pragma unroll 1
     for (int s = 0; s < n; ++s) {
-      const float* src = a.logits + ((size_t)(s0 + s) * a.T + t) * ldp;
+      const float* src = dry ? static_cast<const float*>(a.x) : a.logits + ((size_t)(s0 + s) * a.T + t) * ldp;
 #pragma unroll 1
       for (int c = 4 * lane; c < ldp; c += 128) cp_async16(smem_u32(sc.part + s * ldp + c), src + c);
     }
@@ -383,6 +384,7 @@ __device__ __noinline__ void select_token(const Args& a, Tables& tb, int t) {
   const float sh = a.sink ? sv[N] : 0.f;
   const float sum = warp_sum(s) + sh;
   const float w = r.renorm ? s / sum : s;
+  if (dry) return;
   // the CTA that owns the token writes the outputs
   if (lane < k) {
     if (a.T <= LOCAL_T) {
@@ -403,22 +405,23 @@ __device__ __noinline__ void select_token(const Args& a, Tables& tb, int t) {
 
 // Experts' token masks, met experts in ascending order, rows (expert major, tokens
 // ascending); a token past its expert's capacity gets no row.  By one warp.
-__device__ __noinline__ void build_tables(const Args& a, Tables& tb) {
+// dry (N = 1, n = 1): as if one slot had picked expert 0.
+__device__ __noinline__ void build_tables(const Args& a, Tables& tb, int N, int n, bool dry) {
   Scratch& sc = tb.sc;
-  const int lane = threadIdx.x & 31, n = a.T * a.k;
-  for (int e = lane; e < a.N; e += 32) sc.mask[e][0] = sc.mask[e][1] = 0;
+  const int lane = threadIdx.x & 31;
+  for (int e = lane; e < N; e += 32) sc.mask[e][0] = sc.mask[e][1] = 0;
   if (a.T <= LOCAL_T) {
     if (lane < n) {
-      const int e = sc.el[lane];
-      sc.e[lane] = (unsigned)e < (unsigned)a.N ? (int16_t)e : (int16_t)-1;
+      const int e = dry ? 0 : sc.el[lane];
+      sc.e[lane] = (unsigned)e < (unsigned)N ? (int16_t)e : (int16_t)-1;
       sc.w[lane] = sc.wl[lane];
     }
   } else {                                    // the picks that the grid wrote
 #pragma unroll 4
     for (int s = lane; s < n; s += 32) {
-      const int e = __ldcg(a.topk_idx + s);
-      const float w = __ldcg(a.topk_w + s);
-      sc.e[s] = (unsigned)e < (unsigned)a.N ? (int16_t)e : (int16_t)-1;
+      const int e = dry ? 0 : __ldcg(a.topk_idx + s);
+      const float w = dry ? 0.f : __ldcg(a.topk_w + s);
+      sc.e[s] = (unsigned)e < (unsigned)N ? (int16_t)e : (int16_t)-1;
       sc.w[s] = w;
     }
     if (a.sink)
@@ -429,15 +432,15 @@ __device__ __noinline__ void build_tables(const Args& a, Tables& tb) {
   __syncwarp();
   for (int s = lane; s < n; s += 32) {
     const int e = sc.e[s], t = s / a.k;
-    if ((unsigned)e < (unsigned)a.N) atomicOr(&sc.mask[e][t >> 5], 1u << (t & 31));
+    if ((unsigned)e < (unsigned)N) atomicOr(&sc.mask[e][t >> 5], 1u << (t & 31));
     else flag_invalid_index();
   }
   __syncwarp();
   int rows = 0, act = 0;
 #pragma unroll 1
-  for (int base = 0; base < a.N; base += 32) {
+  for (int base = 0; base < N; base += 32) {
     const int e = base + lane;
-    int c = e < a.N ? __popc(sc.mask[e][0]) + __popc(sc.mask[e][1]) : 0;
+    int c = e < N ? __popc(sc.mask[e][0]) + __popc(sc.mask[e][1]) : 0;
     if (c > a.capacity) c = (int)a.capacity;
     int incl = c;
 #pragma unroll
@@ -446,7 +449,7 @@ __device__ __noinline__ void build_tables(const Args& a, Tables& tb) {
       if (lane >= o) incl += v;
     }
     const unsigned met = __ballot_sync(0xffffffffu, c > 0);
-    if (e < a.N) tb.row0[e + 1] = (int16_t)(rows + incl);
+    if (e < N) tb.row0[e + 1] = (int16_t)(rows + incl);
     if (c > 0) tb.act[act + __popc(met & ((1u << lane) - 1u))] = (int16_t)e;
     rows += __shfl_sync(0xffffffffu, incl, 31);
     act += __popc(met);
@@ -458,7 +461,7 @@ __device__ __noinline__ void build_tables(const Args& a, Tables& tb) {
   __syncwarp();
   for (int s = lane; s < n; s += 32) {
     const int e = sc.e[s], t = s / a.k;
-    if ((unsigned)e >= (unsigned)a.N) continue;
+    if ((unsigned)e >= (unsigned)N) continue;
     const unsigned below = t < 32 ? __popc(sc.mask[e][0] & ((1u << t) - 1u))
                                   : __popc(sc.mask[e][0]) + __popc(sc.mask[e][1] & ((1u << (t - 32)) - 1u));
     if ((int64_t)below < a.capacity) {
@@ -472,10 +475,17 @@ __device__ __noinline__ void build_tables(const Args& a, Tables& tb) {
 // More: token t on CTA t, and all CTAs read the picks when they are there.
 __device__ __forceinline__ void select_and_build(const Args& a, Tables& tb) {
   const int lane = threadIdx.x & 31;
+  // The code comes from memory line by line, longer than its steps take: once through it while
+  // the logits are under way (one token of 256 experts: the tables stand after 16 us instead of
+  // 23, the layer takes 140 us in bf16 instead of 147, 94 in MXFP4 instead of 101).
+  const bool local = a.T <= LOCAL_T;
+  if (local || (int)blockIdx.x < a.T) select_token(a, tb, 0, 1, 1, true);
+  build_tables(a, tb, 1, 1, true);
+  __syncwarp();
   if (lane == 0) grid_wait(a.bar + BAR_LOGITS, gridDim.x, tb);
   __syncwarp();
-  const bool local = a.T <= LOCAL_T;
-  for (int t = local ? 0 : (int)blockIdx.x; t < a.T; t += local ? 1 : (int)gridDim.x) select_token(a, tb, t);
+  for (int t = local ? 0 : (int)blockIdx.x; t < a.T; t += local ? 1 : (int)gridDim.x)
+    select_token(a, tb, t, a.N, a.k, false);
   if (!local) {
     if (lane == 0) {
       if ((int)blockIdx.x < a.T) grid_arrive(a.bar + BAR_PICKS);
@@ -483,7 +493,7 @@ __device__ __forceinline__ void select_and_build(const Args& a, Tables& tb) {
     }
     __syncwarp();
   }
-  build_tables(a, tb);
+  build_tables(a, tb, a.N, a.T * a.k, false);
 }
 
 // ------------------------------------------------------------------ schedule
