@@ -91,6 +91,8 @@ template <class C>
 constexpr int smem_bytes() {
   return 1024 + C::STAGES * stage_bytes<C>() + (C::RED * red_floats<C>() + YACC) * 4 + (int)sizeof(Tables);
 }
+static_assert(alignof(Tables) == 16 && red_floats<Cfg<__nv_bfloat16>>() % 4 == 0 && red_floats<Cfg<Mxfp4>>() % 4 == 0 &&
+              YACC % 4 == 0, "16-byte copies into the tables");
 static_assert(smem_bytes<Cfg<__nv_bfloat16>>() <= 232448 && smem_bytes<Cfg<float>>() <= 232448 &&
               smem_bytes<Cfg<Mxfp4>>() <= 232448, "shared memory per CTA");
 static_assert(8 * ROUTE_COLS <= 2 * red_floats<Cfg<float>>() + YACC && 8 * ROUTE_COLS <= red_floats<Cfg<Mxfp4>>() + YACC,
@@ -193,7 +195,7 @@ struct Gather {
     if (DOWN)
       return reinterpret_cast<const uint8_t*>(static_cast<const XT*>(a.h) + (t.sh ? (size_t)a.T * a.k * a.f : 0) +
                                               (size_t)(t.row + i) * t.K);
-    return reinterpret_cast<const uint8_t*>(static_cast<const XT*>(a.x) +
+    return reinterpret_cast<const uint8_t*>(static_cast<const XT*>(C::MX ? a.x16 : a.x) +
                                             (size_t)(t.sh ? t.row + i : tb.row_tok[t.row + i]) * t.K);
   }
   __device__ __forceinline__ void tile(const Args& a, const Tables& tb, const Tile& t, int xw, int lane) {
@@ -260,6 +262,7 @@ __device__ __forceinline__ void mma_f16(float* d, uint32_t a0, uint32_t a1, uint
                : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
+__device__ __forceinline__ void gather_sync() { asm volatile("bar.sync 2, %0;" ::"n"(32 * X_WARPS) : "memory"); }
 // Two bf16 to fp16, times a power of two.
 __device__ __forceinline__ uint32_t scaled_f16(uint32_t v, float s) {
   const __half2 h = __floats2half2_rn(__uint_as_float(v << 16) * s, __uint_as_float(v & 0xffff0000u) * s);
@@ -285,6 +288,37 @@ template <bool DOWN>
 __device__ __forceinline__ float token_scale(const Tile& t, const Tables& tb, int i) {
   if (DOWN) return tb.hs[t.sh ? MAX_T * MAX_K + t.row + i : t.row + i];
   return tb.xs[t.sh ? t.row + i : tb.row_tok[t.row + i]];
+}
+
+// MXFP4: token t to fp16 on CTA t, once for all that multiply with it (in every product it was
+// a sixth of their instructions), by the warps that gather.
+__device__ __forceinline__ void x_to_f16(const Args& a, Tables& tb, int xw, int lane) {
+  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+    const uint4* row = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.x) + (size_t)t * a.d);
+    uint4* out = reinterpret_cast<uint4*>(static_cast<__half*>(a.x16) + (size_t)t * a.d);
+    uint32_t m = 0;
+#pragma unroll 7
+    for (int c = 32 * xw + lane; c < a.d / 8; c += 32 * X_WARPS) {
+      const uint4 v = ldg_nc16(row + c);
+      m = __vmaxu2(m, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                               __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+    }
+    m = __reduce_max_sync(0xffffffffu, max(m << 16, m & 0xffff0000u));
+    if (lane == 0) tb.xmax[xw] = m;
+    gather_sync();
+    const float s = row_scale(max(tb.xmax[0], tb.xmax[1]));
+#pragma unroll 7
+    for (int c = 32 * xw + lane; c < a.d / 8; c += 32 * X_WARPS) {
+      const uint4 v = ldg_nc16(row + c);
+      out[c] = make_uint4(scaled_f16(v.x, s), scaled_f16(v.y, s), scaled_f16(v.z, s), scaled_f16(v.w, s));
+    }
+    if (xw == 0 && lane == 0) a.xscale[t] = s;
+    __threadfence();
+    gather_sync();
+    if (xw == 0 && lane == 0) grid_arrive(a.bar + BAR_X);
+  }
+  if (lane == 0) grid_wait(a.bar + BAR_X, a.T, tb);
+  __syncwarp();
 }
 
 // This warp's sums over a pass: a 16-row tile by 8 NT tokens on its share of the columns.
@@ -464,10 +498,11 @@ struct Product<Mxfp4, DOWN, NT> {
       for (int n = 0; n < NT; ++n) {
         const uint4 v = lds16(xa + n * 8 * XS + 64 * k);
         // a column without a token holds whatever the stage held before: zeros instead
-        b[k][n][0] = ts[n] > 0.f ? scaled_f16(v.x, ts[n]) : 0u;
-        b[k][n][1] = ts[n] > 0.f ? scaled_f16(v.y, ts[n]) : 0u;
-        b[k][n][2] = ts[n] > 0.f ? scaled_f16(v.z, ts[n]) : 0u;
-        b[k][n][3] = ts[n] > 0.f ? scaled_f16(v.w, ts[n]) : 0u;
+        const bool on = ts[n] > 0.f;
+        b[k][n][0] = !on ? 0u : DOWN ? scaled_f16(v.x, ts[n]) : v.x;
+        b[k][n][1] = !on ? 0u : DOWN ? scaled_f16(v.y, ts[n]) : v.y;
+        b[k][n][2] = !on ? 0u : DOWN ? scaled_f16(v.z, ts[n]) : v.z;
+        b[k][n][3] = !on ? 0u : DOWN ? scaled_f16(v.w, ts[n]) : v.w;
       }
     const uint8_t* wu[BLOCKS];
 #pragma unroll
@@ -718,6 +753,7 @@ few_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps) {
     __syncthreads();
   } else if (warp > W_WARP) {
     // ---------------------------------------------------------------- tokens
+    if constexpr (C::MX) x_to_f16(a, tb, warp - X_WARP0, lane);
     Ring r{0, 0};
     auto stream = [&](auto walk) {
       Tile t;
@@ -747,20 +783,10 @@ few_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps) {
     router_logits<XT>(a, red);
     worker_sync();
     if (tid == 0) grid_arrive(a.bar + BAR_LOGITS);
-    if (C::MX) {                           // each token's largest x, for fp16
-      for (int tok = warp; tok < T; tok += WARPS) {
-        uint32_t m = 0;
-        const uint4* row = reinterpret_cast<const uint4*>(static_cast<const XT*>(a.x) + (size_t)tok * a.d);
-#pragma unroll 4
-        for (int c = lane; c < a.d / 8; c += 32) {
-          float v[8];
-          unpack16(ldg_nc16(row + c), v, __nv_bfloat16());
-#pragma unroll
-          for (int u = 0; u < 8; ++u) m = max(m, __float_as_uint(v[u]) & 0x7fffffffu);
-        }
-        m = __reduce_max_sync(0xffffffffu, m);
-        if (lane == 0) tb.xs[tok] = row_scale(m);
-      }
+    if (C::MX) {
+      if (tid == 0) grid_wait(a.bar + BAR_X, T, tb);
+      worker_sync();
+      if (tid < T) tb.xs[tid] = __ldcg(a.xscale + tid);
       worker_sync();
     }
     if (a.fs > 0)
@@ -833,7 +859,7 @@ cudaError_t launch(const Args& a, const void* const* w, size_t zero, cudaStream_
 
 size_t few_workspace_bytes(const moe_config_t& c, int fs) {
   const size_t eb = c.x_dtype == MOE_DTYPE_F32 ? 4 : 2;
-  return few::zero_bytes(c) + few::shw_bytes(c) + few::logit_bytes(c) +
+  return few::zero_bytes(c) + 2 * few::shw_bytes(c) + few::x16_bytes(c) + few::logit_bytes(c) +
          few::align256(((size_t)c.T * c.top_k * c.d_ff + (size_t)c.T * fs) * eb);
 }
 
@@ -860,6 +886,10 @@ cudaError_t launch_few(const moe_config_t& c, int64_t capacity, const void* x, c
   p += zero;
   a.shw = reinterpret_cast<float*>(p);
   p += few::shw_bytes(c);
+  a.xscale = reinterpret_cast<float*>(p);
+  p += few::shw_bytes(c);
+  a.x16 = p;
+  p += few::x16_bytes(c);
   a.logits = reinterpret_cast<float*>(p);
   a.h = p + few::logit_bytes(c);
   if (mxfp4) return few::launch<few::Mxfp4>(a, w, zero, s);

@@ -16,7 +16,7 @@ constexpr int WORKERS = 16;                     // warps of the router's first p
 constexpr int SLOTS = 64;                       // rows of a down tile
 constexpr int ROUTE_TILE = 16, ROUTE_COLS = 1024;   // router: experts and columns at a time
 constexpr int LOCAL_T = 2;                      // up to here every CTA selects for all tokens
-enum { BAR_LOGITS = 0, BAR_PICKS = 16, BAR_HIDDEN = 32 };
+enum { BAR_LOGITS = 0, BAR_PICKS = 16, BAR_HIDDEN = 32, BAR_X = 48 };
 
 // The six expert stacks [experts * rows, cols]: W1, W3, W2 routed, then shared.
 enum { M_W1 = 0, M_W3 = 1, M_W2 = 2, M_SHARED = 3 };
@@ -35,6 +35,8 @@ struct Args {
   unsigned* hmax;          // MXFP4: [T k + T] largest |h| of each hidden row as bits, zero at launch
   float* shw;              // [T] shared expert's weights (sink)
   float* logits;           // [slices, T, N + sink] partial sums
+  void* x16;               // MXFP4: [T, d] x in fp16, times xscale [T]
+  float* xscale;
   void* h;                 // [T k, f] routed, then [T, fs] shared; x's type
 };
 
@@ -49,7 +51,7 @@ struct Scratch {
     float w[MAX_T * MAX_K];          // then all picks' weights
   };
   union {
-    float part[PART];
+    alignas(16) float part[PART];
     struct {
       int16_t e[MAX_T * MAX_K];      // then all picks
       unsigned mask[MAX_N][2];       // tokens of each expert
@@ -67,6 +69,7 @@ struct Tables {
   float row_w[MAX_T * MAX_K];
   float shw[MAX_T];
   float xs[MAX_T];                   // MXFP4: scale of each token's x
+  uint32_t xmax[2];
   uint64_t full[4], empty[4];
   int32_t n_act;
   volatile int32_t abort;
@@ -595,6 +598,7 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 // weights, logits, hidden rows.
 size_t zero_bytes(const moe_config_t& c) { return align256(256 + (size_t)c.T * (c.top_k + 1) * 4); }
 size_t shw_bytes(const moe_config_t& c) { return align256((size_t)c.T * 4); }
+size_t x16_bytes(const moe_config_t& c) { return align256((size_t)c.T * c.d_model * 2); }
 size_t logit_bytes(const moe_config_t& c) {
   const int ld = c.n_experts + c.shared_sink;
   return align256((size_t)route_slices(ld, c.d_model, (int)c.T) * c.T * route_ld(ld) * 4);
