@@ -47,9 +47,9 @@ struct Maps {
 
 // Per weight type W (fp32 and bf16: x and weights; Mxfp4: bf16 x).  nt: 8-token columns of a
 // pass (1, 2 or 4); seg(nt): columns of a stage.  A stage holds up to 64 weight rows as TMA
-// leaves them (fp32, bf16: row by row, 32 gate rows before 32 up rows; MXFP4, in groups of 8: by 64-byte column chunks, the chunk's 8 rows,
-// 64-byte swizzle, so that the 16 bytes that a quad takes of each of 8 rows fall into
-// different banks), then the tokens' rows, 64 mod 128 bytes apart so that a quarter warp's
+// leaves them (fp32, bf16: row by row, 32 gate rows before 32 up rows; MXFP4, in groups of 8
+// rows: by 64-byte column chunks, the chunk's 8 rows, 64-byte swizzle, so that the 16 bytes
+// that a quad takes of each of 8 rows fall into different banks), then the tokens' rows, 64 mod 128 bytes apart so that a quarter warp's
 // 16-byte reads meet every bank once, then MXFP4's scales, 36 bytes a row.
 // WK warps split a stage's columns, WARPS / WK its 16-row tiles.
 struct Mxfp4 {};
@@ -457,7 +457,7 @@ struct Product<float, DOWN, NT> {
 // the conversion of 4-bit codes, where HBM would allow 47 at one a clock.  The block-scaled
 // tensor cores take the codes as they are, but not at this shape: an M = 128 x K = 32 MMA
 // costs ~200 cycles however few tokens there are, 800 for the 8.7 KB of codes that HBM
-// brings in 357 (measured with that kernel: 1.93 ms for 24 tokens against this one's 1.06).
+// brings in 357 (measured with that kernel: 1.93 ms for 24 tokens against this one's 1.02).
 template <bool DOWN, int NT>
 struct Product<Mxfp4, DOWN, NT> {
   using C = Cfg<Mxfp4>;
@@ -560,6 +560,9 @@ __device__ __forceinline__ void run_pass(const Args& a, Tables& tb, const Tile& 
   for (int n = 0; n < NT; ++n) {
     if (8 * n >= t.n) break;
     float* rb = red + buf * red_floats<C>();
+    // one buffer: the sums before these have been read (a meeting here and not after the reads
+    // lets the warps that read nothing go on with the next tile: 1040 -> 1017 us for 24 tokens)
+    if (C::RED == 1) worker_sync();
 #pragma unroll
     for (int q = 0; q < p.QT; ++q) {
       float c[4];
@@ -615,7 +618,6 @@ __device__ __forceinline__ void run_pass(const Args& a, Tables& tb, const Tile& 
       }
     }
     if (C::RED == 2) buf ^= 1;
-    else worker_sync();
   }
 }
 
