@@ -714,7 +714,8 @@ int moe_combine(const moe_config_t* cfg, const void* y_perm, const int32_t* row_
  *               blocks wait on: calls that may overlap on the GPU (two streams, two
  *               replayed graphs) need a workspace each.
  * The launch is cooperative, one block on every SM; it starts when all of them are free.
- * Errors: MOE_ERR_UNSUPPORTED for T > 64; MOE_ERR_INVALID_ARG for a bad config, a bad
+ * Errors: MOE_ERR_UNSUPPORTED for T > 64, or N * f or N * d past 2^31 - 1 (rows of a
+ * weight stack are 32-bit coordinates); MOE_ERR_INVALID_ARG for a bad config, a bad
  * f_shared, or a NULL or misaligned (16-byte; 4-byte for [N] and [T, k] arrays) buffer;
  * MOE_ERR_WORKSPACE_TOO_SMALL.
  * ------------------------------------------------------------------------- */

@@ -128,7 +128,7 @@ int few_tokens(const moe_config_t* cfg, const void* x, const float* w_gate, cons
        reinterpret_cast<uintptr_t>(logit_offset) | reinterpret_cast<uintptr_t>(bias)) & 3u)
     return MOE_ERR_INVALID_ARG;
   for (int i = 0; i < (f_shared > 0 ? 6 : 3); ++i)
-    if (!w[i] || !aligned16(w[i]) || (mxfp4 && (!aligned32(w[i]) || !sf[i] || !aligned16(sf[i]))))
+    if (!w[i] || !aligned16(w[i]) || (mxfp4 && (!sf[i] || !aligned16(sf[i]))))
       return MOE_ERR_INVALID_ARG;
   if (ws_bytes < few_workspace_bytes(*cfg, f_shared)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   if (!ws || !aligned16(ws)) return MOE_ERR_INVALID_ARG;

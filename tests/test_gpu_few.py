@@ -379,3 +379,21 @@ def test_mxfp4_scale_byte_zero_counts():
     # y rounds to bf16 (2^-8 of itself); h may round the other way (2^-7 of one step of h): with
     # the sums' fp32 error far below, 2^-6 of the row's norm bounds both
     assert float((y.double() - ref).norm()) <= 2.0 ** -6 * float(ref.norm())
+
+
+def test_mxfp4_codes_at_16_byte_addresses():
+    """Codes that start 16 bytes into an allocation: the same results as aligned ones."""
+    f = Few(replace(WORKLOADS["deepseekmoe_16b"], T=5, N=8, d=256, f=128, n_shared=1, f_shared=128), mxfp4=True)
+    f.call()
+    y = f.y.clone()
+    keep = []
+    for n, (q, sf) in f.mats.items():
+        buf = torch.zeros(q.numel() + 64, dtype=torch.uint8, device="cuda")
+        view = buf[16:16 + q.numel()].view(q.shape)
+        view.copy_(q)
+        assert view.data_ptr() % 32 == 16
+        keep.append(buf)
+        f.mats[n] = (view, sf)
+    f.y.fill_(7.0)
+    f.call()
+    assert torch.equal(f.y, y)
