@@ -694,7 +694,7 @@ int moe_combine(const moe_config_t* cfg, const void* y_perm, const int32_t* row_
  * Defines: the layer of the calls above (route, capacity drop, experts, shared expert,
  * weighted sum), as a step of token-by-token serving needs it: with few tokens the
  * layer is bound by the bytes of the picked experts' weights, and every weight is read
- * once.  Selection, ties, capacity and weights are moe_route's and moe_permute's
+ * once (once for each 32 of an expert's tokens).  Selection, ties, capacity and weights are moe_route's and moe_permute's
  * (logits in fp32); for each token
  *   y = shared_weight * shared(x) + sum over its kept picks of w * E(x),
  * E(x) = W2 (silu(W1 x) * (W3 x)), the hidden row rounded to x's type, every sum in
@@ -714,10 +714,10 @@ int moe_combine(const moe_config_t* cfg, const void* y_perm, const int32_t* row_
  *               blocks wait on: calls that may overlap on the GPU (two streams, two
  *               replayed graphs) need a workspace each.
  * The launch is cooperative, one block on every SM; it starts when all of them are free.
- * Errors: MOE_ERR_UNSUPPORTED for T > 64, or N * f or N * d past 2^31 - 1 (rows of a
- * weight stack are 32-bit coordinates); MOE_ERR_INVALID_ARG for a bad config, a bad
- * f_shared, or a NULL or misaligned (16-byte; 4-byte for [N] and [T, k] arrays) buffer;
- * MOE_ERR_WORKSPACE_TOO_SMALL.
+ * Errors: MOE_ERR_UNSUPPORTED for T > 64, for d, f or f_shared past 2^24, or for N * f or
+ * N * d past 2^31 - 1 (rows of a weight stack are 32-bit coordinates);
+ * MOE_ERR_INVALID_ARG for a bad config, a bad f_shared, or a NULL or misaligned (16-byte;
+ * 4-byte for [N] and [T, k] arrays) buffer; MOE_ERR_WORKSPACE_TOO_SMALL.
  * ------------------------------------------------------------------------- */
 int moe_few_tokens_workspace_size(const moe_config_t* cfg, int32_t f_shared, size_t* bytes);
 int moe_few_tokens(const moe_config_t* cfg, const void* x, const float* w_gate, const float* logit_offset,

@@ -106,6 +106,9 @@ int check_few(const moe_config_t* cfg, int32_t f_shared, bool mxfp4) {
   if (st != MOE_OK) return st;
   if (cfg->d_ff <= 0 || (cfg->d_ff % 8) != 0 || f_shared < 0 || (f_shared % 8) != 0) return MOE_ERR_INVALID_ARG;
   if (cfg->T > 64) return MOE_ERR_UNSUPPORTED;
+  // byte offsets within a row are 32 bits
+  constexpr int kMaxWidth = 1 << 24;
+  if (cfg->d_model > kMaxWidth || cfg->d_ff > kMaxWidth || f_shared > kMaxWidth) return MOE_ERR_UNSUPPORTED;
   // rows of an expert stack are 32-bit coordinates
   if ((int64_t)cfg->n_experts * cfg->d_ff > (int64_t)INT32_MAX ||
       (int64_t)cfg->n_experts * cfg->d_model > (int64_t)INT32_MAX)

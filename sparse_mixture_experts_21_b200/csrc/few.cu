@@ -4,7 +4,8 @@
 //   y_t = sum_j w_tj W2_e (silu(W1_e x_t) * (W3_e x_t)) + shared(x_t)
 //
 // Bound: the bytes of the weights of the experts that at least one token picks (and of the
-// router and the shared expert); every weight is read once, from HBM.
+// router and the shared expert); every weight is read once from HBM, or once for each 32 of an
+// expert's tokens (all CTAs' tiles together outgrow the L2 before the next 32 need them).
 //
 // One cooperative launch, one CTA per SM, barriers over the grid:
 //   logits     spread over the grid in K slices; arrive at barrier 1

@@ -106,3 +106,12 @@ def test_layer_refuses():
         lp.w, lp.weights = replace(V3, **{flag: True}), {}
         with pytest.raises(ValueError):
             lp.forward_few(torch.zeros(2, 7168))
+
+
+def test_widths_past_the_offsets(lib):
+    one = dict(N=1, k=1, n_groups=1, topk_groups=1, group_topn=1)
+    big = (1 << 24) + 128
+    assert call(lib, w=replace(V3, d=big, **one)) == UN
+    assert call(lib, w=replace(V3, f=big, **one)) == UN
+    assert call(lib, w=replace(V3, **one), fs=big) == UN
+    assert call(lib, w=replace(V3, N=256, f=1 << 23)) == UN            # rows of a stack past 2^31
