@@ -167,7 +167,8 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 def _stream(stream=None) -> Optional[int]:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the handle alone: a Stream object around it costs 3 us of a call's 11
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream
 
 
