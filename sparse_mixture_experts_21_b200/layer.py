@@ -6,6 +6,7 @@ stream); every step runs in the library's kernels.
 """
 from __future__ import annotations
 
+from contextlib import nullcontext
 from typing import Optional
 
 import torch
@@ -330,20 +331,28 @@ class MoELayer:
         [n, k].  With MXFP4 experts x and the hidden rows stay bf16 (forward quantises
         them to MXFP8).  Writes no statistics and updates no bias.  Calls of one layer
         share its scratch, so they must be ordered on the GPU; the first call allocates
-        it (make it before a capture)."""
+        it (make it before a capture).  stream: where the launch goes (the current one if
+        None); the caller orders it after what writes x and before what reads y."""
         w, W, n = self.w, self.weights, x.shape[0]
         if w.expert_choice or w.fp8 or w.mxfp8 or w.nvfp4:
             raise ValueError("forward_few runs token-choice routing over bf16, fp32 or MXFP4 experts")
         if x.dim() != 2 or x.shape[1] != w.d or n > L.FEW_TOKENS_MAX:
             raise ValueError(f"forward_few takes [n, {w.d}] with n <= {L.FEW_TOKENS_MAX}, not {list(x.shape)}")
-        if not hasattr(self, "_few"):
-            c = make_config(w, L.FEW_TOKENS_MAX)
-            self._few = {"ws": torch.empty(L.few_tokens_workspace_size(c, self.fs), dtype=torch.uint8, device=self.dev),
-                         "idx": torch.empty(L.FEW_TOKENS_MAX, w.k, dtype=torch.int32, device=self.dev),
-                         "w": torch.empty(L.FEW_TOKENS_MAX, w.k, device=self.dev), "cfg": {}}
+        # memory from the pool of the stream that writes it: a block of the current stream's
+        # may still be in use by that stream's earlier work, or be handed out again before
+        # another stream's launch has written it
+        with nullcontext() if stream is None else torch.cuda.stream(stream):
+            if not hasattr(self, "_few"):
+                c = make_config(w, L.FEW_TOKENS_MAX)
+                self._few = {"ws": torch.empty(L.few_tokens_workspace_size(c, self.fs), dtype=torch.uint8,
+                                               device=self.dev),
+                             "idx": torch.empty(L.FEW_TOKENS_MAX, w.k, dtype=torch.int32, device=self.dev),
+                             "w": torch.empty(L.FEW_TOKENS_MAX, w.k, device=self.dev), "cfg": {}}
+            y = torch.empty_like(x) if out is None else out
+        if stream is not None and out is None:
+            y.record_stream(torch.cuda.current_stream(self.dev))       # read there
         B = self._few
         c = B["cfg"].setdefault(n, make_config(w, n))
-        y = torch.empty_like(x) if out is None else out
         self.few_idx, self.few_w = B["idx"][:n], B["w"][:n]
         names = ("w1", "w3", "w2", "ws1", "ws3", "ws2")
         fn, src = (L.moe_few_tokens_mxfp4, self.wq) if w.mxfp4 else (L.moe_few_tokens, W)
