@@ -352,7 +352,9 @@ class MoELayer:
         if stream is not None and out is None:
             y.record_stream(torch.cuda.current_stream(self.dev))       # read there
         B = self._few
-        c = B["cfg"].setdefault(n, make_config(w, n))
+        c = B["cfg"].get(n)
+        if c is None:
+            c = B["cfg"][n] = make_config(w, n)
         self.few_idx, self.few_w = B["idx"][:n], B["w"][:n]
         names = ("w1", "w3", "w2", "ws1", "ws3", "ws2")
         fn, src = (L.moe_few_tokens_mxfp4, self.wq) if w.mxfp4 else (L.moe_few_tokens, W)

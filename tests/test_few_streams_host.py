@@ -72,3 +72,15 @@ def test_a_given_output_is_used_as_it_is(monkeypatch):
     n, out = len(h.allocated), torch.zeros(3, W.d)
     assert h.lay.forward_few(torch.zeros(3, W.d), "side", out=out) is out
     assert len(h.allocated) == n and not h.recorded
+
+
+def test_the_configuration_is_built_once_per_count(monkeypatch):
+    """A latency-bound call builds nothing that the call before has left."""
+    h = Host(monkeypatch)
+    built = []
+    real = layer.make_config
+    monkeypatch.setattr(layer, "make_config", lambda w, T=None: built.append(T) or real(w, T))
+    for n in (3, 3, 5, 3, 5):
+        h.lay.forward_few(torch.zeros(n, W.d))
+    assert built == [L.FEW_TOKENS_MAX, 3, 5]
+    assert [c.T for c, _ in h.launched] == [3, 3, 5, 3, 5]
