@@ -328,7 +328,9 @@ def moe_grouped_ffn_mxfp8(cfg, xq_rows, xsf_rows, rows_cap, offsets, G, w1q, w1s
 
 
 def _expect(name: str, t: torch.Tensor, dtype: torch.dtype, numel: int, device=None) -> None:
-    """Refuse a buffer of another type or device, or one too small for what is written or read."""
+    """Refuse a missing buffer, one of another type or device, or one too small for what is written or read."""
+    if t is None:
+        raise ValueError(f"{name} is missing")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
     if t.numel() < numel:
@@ -338,6 +340,8 @@ def _expect(name: str, t: torch.Tensor, dtype: torch.dtype, numel: int, device=N
 
 
 def _float_type(name: str, t: torch.Tensor) -> int:
+    if t is None:
+        raise ValueError(f"{name} is missing")
     if t.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError(f"{name} must be float32 or bfloat16, not {t.dtype}")
     return DTYPE_F32 if t.dtype == torch.float32 else DTYPE_BF16
@@ -347,8 +351,8 @@ def moe_quantize_mxfp4(x, q, sf, stream=None):
     """MXFP4-quantise an fp32 or bf16 matrix [rows, cols] along its rows: packed E2M1 codes
     (q: rows x cols / 2 bytes) and E8M0 scales (sf from mx_scales(rows, cols)).  Runs on x's
     device."""
-    rows, cols = x.shape
     dt = _float_type("x", x)
+    rows, cols = x.shape
     if cols % 128 == 0:
         _expect("q", q, torch.uint8, rows * cols // 2, x.device)
         _expect("sf", sf, torch.uint8, (rows + 127) // 128 * cols * 4, x.device)
@@ -360,8 +364,8 @@ def moe_quantize_mxfp4(x, q, sf, stream=None):
 def moe_dequantize_mxfp4(q, sf, y, stream=None):
     """y [rows, cols] (fp32 or bf16) = the values that codes q and scales sf stand for.  Runs on
     y's device."""
-    rows, cols = y.shape
     dt = _float_type("y", y)
+    rows, cols = y.shape
     if cols % 128 == 0:
         _expect("q", q, torch.uint8, rows * cols // 2, y.device)
         _expect("sf", sf, torch.uint8, (rows + 127) // 128 * cols * 4, y.device)
@@ -492,9 +496,10 @@ def few_tokens_workspace_size(cfg: MoeConfig, f_shared: int = 0) -> int:
 
 
 def _few_check(cfg, x, w_gate, logit_offset, bias, weights, sizes, wtype, topk_idx, topk_w, y, ws):
-    T, N, k, d, dev = cfg.T, cfg.n_experts, cfg.top_k, cfg.d_model, x.device
+    T, N, k, d = cfg.T, cfg.n_experts, cfg.top_k, cfg.d_model
     xt = torch.float32 if cfg.x_dtype == DTYPE_F32 else torch.bfloat16
     _expect("x", x, xt, T * d)
+    dev = x.device
     _expect("y", y, xt, T * d, dev)
     _expect("w_gate", w_gate, torch.float32, (N + cfg.shared_sink) * d, dev)
     for name, t in (("logit_offset", logit_offset), ("bias", bias)):
