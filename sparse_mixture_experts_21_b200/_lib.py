@@ -376,8 +376,26 @@ def moe_dequantize_mxfp4(q, sf, y, stream=None):
 
 def moe_grouped_ffn_mxfp4(cfg, xq_rows, xsf_rows, rows_cap, offsets, G, w1q, w1sf, w3q, w3sf, w2q, w2sf, f,
                           hq_scratch, hsf_scratch, y_rows, stream=None):
-    """moe_grouped_ffn_mxfp8 with MXFP4 weights (packed codes from moe_quantize_mxfp4)."""
-    with torch.cuda.device(y_rows.device):
+    """moe_grouped_ffn_mxfp8 with MXFP4 weights (packed codes from moe_quantize_mxfp4); scales of
+    rows from mx_scales(rows_cap, d or f, device, G).  Runs on xq_rows' device."""
+    R, G, f, d, u8 = int(rows_cap), int(G), int(f), cfg.d_model, torch.uint8
+    e4m3 = [u8 if t is None or t.dtype != torch.float8_e4m3fn else t.dtype for t in (xq_rows, hq_scratch)]
+    _expect("xq_rows", xq_rows, e4m3[0], max(R, 0) * d)
+    dev = xq_rows.device
+    if R > 0 and G > 0 and d % 128 == 0 and f % 128 == 0:     # else the library's to refuse
+        # any split of R rows into G groups fits: most tiles when all groups but one hold a row
+        m = min(G, R)
+        tiles = m + (R - m) // 128
+        _expect("xsf_rows", xsf_rows, u8, tiles * d * 4, dev)
+        _expect("offsets", offsets, torch.int32, G + 1, dev)
+        for name, q, sf, rows, cols in (("w1", w1q, w1sf, G * f, d), ("w3", w3q, w3sf, G * f, d),
+                                        ("w2", w2q, w2sf, G * d, f)):
+            _expect(name + "q", q, u8, rows * cols // 2, dev)
+            _expect(name + "sf", sf, u8, rows // 128 * cols * 4, dev)
+        _expect("hq_scratch", hq_scratch, e4m3[1], R * f, dev)
+        _expect("hsf_scratch", hsf_scratch, u8, tiles * f * 4, dev)
+        _expect("y_rows", y_rows, torch.bfloat16, R * d, dev)
+    with torch.cuda.device(dev):
         _check("moe_grouped_ffn_mxfp4", load().moe_grouped_ffn_mxfp4(
             ctypes.byref(cfg), _ptr(xq_rows), _ptr(xsf_rows), int(rows_cap), _ptr(offsets), int(G), _ptr(w1q),
             _ptr(w1sf), _ptr(w3q), _ptr(w3sf), _ptr(w2q), _ptr(w2sf), int(f), _ptr(hq_scratch), _ptr(hsf_scratch),

@@ -2,6 +2,7 @@
 library (no GPU)."""
 from __future__ import annotations
 
+from contextlib import nullcontext
 from dataclasses import replace
 
 import pytest
@@ -47,3 +48,71 @@ def test_quantise_refuses_a_missing_operand(at):
         L.moe_quantize_mxfp4(*args)
     with pytest.raises(ValueError):
         L.moe_dequantize_mxfp4(args[1], args[2], args[0])
+
+
+# ------------------------------------------------------------------ the grouped product
+def ffn_args(G=3, rows=200, d=256, f=128):
+    u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8)  # noqa: E731
+    scales = lambda r, c, g=0: L.mx_scales(r, c, "cpu", g)  # noqa: E731
+    cfg = layer.make_config(replace(synth.WORKLOADS["deepseek_v3"], d=d, T=rows))
+    return cfg, dict(xq=u8(rows, d), xsf=scales(rows, d, G), rows=rows, off=torch.zeros(G + 1, dtype=torch.int32), G=G,
+                     w1=u8(G * f, d // 2), s1=scales(G * f, d), w3=u8(G * f, d // 2), s3=scales(G * f, d),
+                     w2=u8(G * d, f // 2), s2=scales(G * d, f), f=f, h=u8(rows, f), hs=scales(rows, f, G),
+                     y=torch.zeros(rows, d, dtype=torch.bfloat16))
+
+
+class Reached(Exception):
+    pass
+
+
+@pytest.fixture
+def reach(monkeypatch):
+    """The binding's checks alone: what passes them ends here instead of in the library."""
+    def load():
+        raise Reached
+    monkeypatch.setattr(L, "load", load)
+    monkeypatch.setattr(torch.cuda, "device", lambda d: nullcontext())
+
+    def call(cfg, a):
+        L.moe_grouped_ffn_mxfp4(cfg, *a.values())
+    return call
+
+
+def test_grouped_ffn_refuses_operands_that_do_not_fit(reach):
+    """Every operand short by its smallest step, of another type, missing, or elsewhere."""
+    for name in ("xq", "xsf", "off", "w1", "s1", "w3", "s3", "w2", "s2", "h", "hs", "y"):
+        cfg, a = ffn_args()
+        if name in ("xsf", "hs"):       # buffers for any split: at worst 2 groups of 1 row and one of 198
+            per = 512 * (256 if name == "xsf" else 128) // 128
+            short = a[name][:4 * per - 1]
+        else:
+            short = a[name].reshape(-1)[:-1]
+        other = a[name].to(torch.int64 if name == "off" else torch.float16)
+        for bad in (short, other, None, a[name].to("meta")):
+            with pytest.raises(ValueError):
+                reach(cfg, dict(a, **{name: bad}))
+
+
+@pytest.mark.parametrize("G,rows", [(1, 1), (1, 128), (1, 129), (3, 2), (3, 200), (5, 700), (64, 509)])
+def test_grouped_ffn_takes_scale_buffers_that_hold_every_split(reach, G, rows):
+    """The fewest 128-row tiles that hold any split of the rows into groups are enough (a plain
+    matrix's for one group); one atom less is refused."""
+    cfg, a = ffn_args(G, rows)
+    # most tiles: as many groups as there are rows for hold one row, the rest fills whole tiles
+    worst = max((m + (rows - m) // 128 for m in range(1, min(G, rows) + 1)))
+    for name, cols in (("xsf", 256), ("hs", 128)):
+        need = worst * cols // 128 * 512
+        with pytest.raises(Reached):
+            reach(cfg, dict(a, **{name: torch.zeros(need, dtype=torch.uint8)}))
+        with pytest.raises(ValueError):
+            reach(cfg, dict(a, **{name: torch.zeros(need - 512, dtype=torch.uint8)}))
+    if G == 1:
+        assert L.mx_scales(rows, 256, "cpu").numel() == worst * 2 * 512
+
+
+def test_grouped_ffn_takes_rows_of_the_8_bit_type(reach):
+    cfg, a = ffn_args()
+    for n in ("xq", "h"):
+        a[n] = a[n].view(torch.float8_e4m3fn)
+    with pytest.raises(Reached):
+        reach(cfg, a)
