@@ -539,6 +539,118 @@ struct Product<Mxfp4, DOWN, NT> {
   }
 };
 
+// ------------------------------------------------------------------ range (MXFP4)
+// The products multiply a row that is scaled to [2^14, 2^15) by the block scales and divide by the
+// row's scale at the end: under block scales from about 2^105 the sum leaves fp32 on the way
+// although it may be an ordinary number.  Dividing first would cost each block of each product
+// four multiplications.  So what came out not finite is formed again when the phase is over, the
+// factors in an order that leaves fp32 only where the sum does; finite results cost a comparison
+// each.  (A scale byte 255 is NaN here; the products, for which it is an infinity, end up here
+// with it.)  A row that holds an infinity or a NaN itself keeps what the products gave.
+__device__ __forceinline__ bool finite_row(float scale) {        // row_scale(255 << 23): exponent field 13
+  return (__float_as_uint(scale) >> 23) != 13u;
+}
+// Row `row` of a stack times v, whose scale is s, by one warp.
+__device__ __noinline__ float dot_in_range(const uint8_t* q, const uint8_t* sf, int row, int K, const __nv_bfloat16* v,
+                                           float s) {
+  const int lane = threadIdx.x & 31;
+  const float inv = inverse_pow2(s);
+  const uint4* codes = reinterpret_cast<const uint4*>(q + (size_t)row * (K / 2));
+  const uint4* x = reinterpret_cast<const uint4*>(v);
+  float sum = 0.f;
+#pragma unroll 1
+  for (int b = lane; b < K / 32; b += 32) {
+    const uint4 w = ldg_nc16(codes + b);
+    const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+    float p = 0.f;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      uint32_t c[4];
+      mx4::e2m1_f16(words[u], c);
+      float xf[8];
+      unpack16(__ldcg(x + 4 * b + u), xf, __nv_bfloat16());
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 cf = __half22float2(*reinterpret_cast<const __half2*>(&c[i]));
+        p = fmaf(cf.x, xf[2 * i] * s, p);
+        p = fmaf(cf.y, xf[2 * i + 1] * s, p);
+      }
+    }
+    const uint32_t sb = sf[mx::atom_byte(row >> 7, K / 128, b >> 2, row & 127, b & 3)];
+    sum = fmaf(p, mx4::e8m0_value(sb) * fminf(inv, 1.f), sum);
+  }
+  return warp_sum(sum) * fmaxf(inv, 1.f);
+}
+__device__ __forceinline__ float swiglu(float gate, float up) { return gate / (1.f + expf(-gate)) * up; }
+
+// This CTA's hidden units of the shared or the routed part that are not finite, by the consumer
+// warps (a token each); their share of the rows' maxima, which the tiles left out.
+__device__ __noinline__ void hidden_in_range(const Args& a, const Tables& tb, bool shared) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const size_t routed = (size_t)a.T * a.k * a.f;
+  Tile t;
+  for (Walk<Cfg<Mxfp4>, false> w(a, tb, shared); w.next(t);)
+    for (int i = warp; i < t.n; i += WARPS) {
+      const int tok = t.sh ? t.row + i : tb.row_tok[t.row + i];
+      const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.x) + (size_t)tok * a.d;
+      __nv_bfloat16* h = static_cast<__nv_bfloat16*>(a.h) + (t.sh ? routed : 0) +
+                         (size_t)(t.row + i) * (t.sh ? a.fs : a.f) + t.base;
+      static_assert(8 * Cfg<Mxfp4>::GATE_UNITS == 32, "a lane per unit");
+      float v = lane < 8 * t.nu ? __bfloat162float(__ldcg(h + lane)) : 0.f;
+      const bool bad = !isfinite(v);
+      const float s = tb.xs[tok];
+      for (unsigned m = finite_row(s) ? __ballot_sync(0xffffffffu, bad) : 0u; m; m &= m - 1) {
+        const int src = __ffs(m) - 1, row = t.erow + t.base + src;
+        const float gate = dot_in_range(a.q[t.ma], a.sf[t.ma], row, t.K, x, s);
+        const float up = dot_in_range(a.q[t.mb], a.sf[t.mb], row, t.K, x, s);
+        if (lane == src) {
+          const __nv_bfloat16 hx = __float2bfloat16_rn(swiglu(gate, up));
+          h[lane] = hx;
+          v = __bfloat162float(hx);
+        }
+      }
+      if (bad) atomicMax(a.hmax + (t.sh ? a.T * a.k : 0) + t.row + i, __float_as_uint(fabsf(v)));
+    }
+}
+
+// Output j of token tok, by one warp; v: what the products gave.
+__device__ __noinline__ float output_in_range(const Args& a, const Tables& tb, int tok, int j, float v) {
+  const __nv_bfloat16* h = static_cast<const __nv_bfloat16*>(a.h);
+  float sum = 0.f;
+  if (a.fs > 0) {
+    const float s = tb.hs[MAX_T * MAX_K + tok];
+    if (!finite_row(s)) return v;
+    sum = tb.shw[tok] * dot_in_range(a.q[M_W2 + M_SHARED], a.sf[M_W2 + M_SHARED], j, a.fs,
+                                     h + (size_t)a.T * a.k * a.f + (size_t)tok * a.fs, s);
+  }
+#pragma unroll 1
+  for (int i = 0; i < tb.n_act; ++i) {
+    const int e = tb.act[i];
+#pragma unroll 1
+    for (int r = tb.row0[e]; r < tb.row0[e + 1]; ++r) {
+      if (tb.row_tok[r] != tok) continue;
+      if (!finite_row(tb.hs[r])) return v;
+      sum = fmaf(tb.row_w[r], dot_in_range(a.q[M_W2], a.sf[M_W2], e * a.d + j, a.f, h + (size_t)r * a.f, tb.hs[r]), sum);
+    }
+  }
+  return sum;
+}
+// This CTA's outputs that are not finite, by the consumer warps (a token each).
+__device__ __noinline__ void outputs_in_range(const Args& a, const Tables& tb) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Walk<Cfg<Mxfp4>, true> w(a, tb, false);
+  for (int tok = warp; tok < a.T; tok += WARPS)
+    for (int j0 = 8 * w.u; j0 < 8 * w.u1; j0 += 32) {
+      __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + (size_t)tok * a.d + j0;
+      const float v = j0 + lane < 8 * w.u1 ? __bfloat162float(__ldcg(y + lane)) : 0.f;
+      for (unsigned m = __ballot_sync(0xffffffffu, !isfinite(v)); m; m &= m - 1) {
+        const int src = __ffs(m) - 1;
+        const float again = output_in_range(a, tb, tok, j0 + src, __shfl_sync(0xffffffffu, v, src));
+        if (lane == src) y[lane] = __float2bfloat16_rn(again);
+      }
+    }
+}
+
 // One tile pass: all its stages, then the warps' partial sums through shared memory and the
 // tile's results.  gate/up: h = silu(gate) * up to memory; down: weighted sums into yacc.
 template <typename W, bool DOWN, int NT>
@@ -608,10 +720,14 @@ __device__ __forceinline__ void run_pass(const Args& a, Tables& tb, const Tile& 
         }
         // the hidden row is rounded to x's type, as the rows of the other forms are: 2^-9 of a
         // value on average, beside the 2^-9 of the output's own rounding
-        const XT hx = (XT)(gate / (1.f + expf(-gate)) * up);
+        const XT hx = (XT)swiglu(gate, up);
         XT* hr = static_cast<XT*>(a.h) + (t.sh ? (size_t)a.T * a.k * a.f : 0);
         hr[(size_t)(t.row + i) * (t.sh ? a.fs : a.f) + j] = hx;
         h = fabsf((float)hx);
+        if (C::MX && !isfinite(h)) {             // a sum that is not finite leaves no finite h
+          tb.redo[0] = 1;
+          h = 0.f;
+        }
       }
       if (C::MX) {                               // the row's largest, for the down pass's fp16
         const unsigned m = __reduce_max_sync(0xffffffffu, __float_as_uint(h));
@@ -687,6 +803,7 @@ __device__ __forceinline__ void run_down_by_token(const Args& a, Tables& tb, Wal
 #pragma unroll
         for (int k = 0; k < C::WK; ++k) v += red[(k * 8 + tok) * RED_LD + (tid & 63) + 16];
       y[(size_t)tok * a.d + j] = (XT)v;
+      if (C::MX && !isfinite(v)) tb.redo[1] = 1;
     }
     worker_sync();
   }
@@ -715,6 +832,7 @@ few_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps) {
     }
     tb.abort = 0;
     tb.n_act = 0;
+    tb.redo[0] = tb.redo[1] = 0;
     fence_barrier_init();
   }
   __syncthreads();
@@ -799,6 +917,12 @@ few_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps) {
     // this CTA's hidden rows to the grid
     __threadfence();
     worker_sync();
+    if (C::MX && tb.redo[0]) {
+      if (a.fs > 0) hidden_in_range(a, tb, true);
+      hidden_in_range(a, tb, false);
+      __threadfence();
+      worker_sync();
+    }
     if (tid == 0) {
       grid_arrive(a.bar + BAR_HIDDEN);
       if (C::MX) grid_wait(a.bar + BAR_HIDDEN, gridDim.x, tb);
@@ -826,10 +950,12 @@ few_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps) {
       for (int i = tid; i < T * SLOTS; i += CONSUMERS) {
         const int j = slot_row<true>(t, i & (SLOTS - 1));
         if (j >= 0) y[(size_t)(i / SLOTS) * a.d + j] = (XT)yacc[i];
+        if (C::MX && !isfinite(yacc[i])) tb.redo[1] = 1;
         yacc[i] = 0.f;
       }
       worker_sync();
     }
+    if (C::MX && tb.redo[1]) outputs_in_range(a, tb);
   }
 }
 
@@ -873,7 +999,10 @@ cudaError_t launch_few(const moe_config_t& c, int64_t capacity, const void* x, c
   few::Args a{};
   a.x = x;
   a.w_gate = w_gate;
-  for (int i = 0; i < 6; ++i) a.sf[i] = mxfp4 ? sf[i] : nullptr;
+  for (int i = 0; i < 6; ++i) {
+    a.q[i] = mxfp4 ? static_cast<const uint8_t*>(w[i]) : nullptr;
+    a.sf[i] = mxfp4 ? sf[i] : nullptr;
+  }
   a.T = (int)c.T; a.d = c.d_model; a.f = c.d_ff; a.fs = fs; a.N = c.n_experts; a.k = c.top_k; a.sink = c.shared_sink;
   a.capacity = capacity;
   a.route = rt::RouteArgs{logit_offset, bias, c.T, c.n_experts, c.top_k, c.score_fn, c.renorm, c.n_groups,

@@ -24,7 +24,8 @@ enum { M_W1 = 0, M_W3 = 1, M_W2 = 2, M_SHARED = 3 };
 struct Args {
   const void* x;
   const float* w_gate;
-  const uint8_t* sf[6];    // MXFP4: tile-atom scales of the stacks
+  const uint8_t* q[6];     // MXFP4: codes of the stacks
+  const uint8_t* sf[6];    // and their tile-atom scales
   int T, d, f, fs, N, k, sink;
   int64_t capacity;
   rt::RouteArgs route;     // selection options
@@ -73,6 +74,7 @@ struct Tables {
   uint64_t full[4], empty[4];
   int32_t n_act;
   volatile int32_t abort;
+  int32_t redo[2];                   // MXFP4: this CTA's hidden rows or outputs hold some that are not finite
   union {
     Scratch sc;                      // while selecting
     float hs[MAX_T * MAX_K + MAX_T]; // then, MXFP4: scale of each hidden row
