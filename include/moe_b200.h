@@ -729,7 +729,7 @@ int moe_few_tokens(const moe_config_t* cfg, const void* x, const float* w_gate, 
  * as moe_quantize_mxfp4 writes them (rows = N * f or N * d).  x and the hidden rows stay
  * bf16: with few tokens their bytes do not count, so they are not quantised as
  * moe_grouped_ffn_mxfp4's rows are.  Scales of any size are taken: a result that lies within
- * fp32's range is finite however large its blocks and small its rows.
+ * fp32's range is finite however large its blocks and small its rows; a scale byte 255 is NaN.
  * Errors: as moe_few_tokens; MOE_ERR_UNSUPPORTED unless a bf16 config with d, f and
  * f_shared multiples of 128. */
 int moe_few_tokens_mxfp4(const moe_config_t* cfg, const void* x, const float* w_gate, const float* logit_offset,

@@ -114,3 +114,30 @@ def test_small_weights_of_small_hidden_rows_under_large_blocks(T):
     few = Few(w, mxfp4=True, inp=inp)
     few.call()
     few.check(routing=False)          # affinities of 2^-20 are all near ties to the routing check
+
+
+@pytest.mark.parametrize("T", [3, 12])
+def test_a_nan_scale_over_nonzero_codes_is_nan(T):
+    """Scale bytes of 255 that another quantiser may leave over nonzero codes: NaN, as
+    moe_dequantize_mxfp4 reads them, in what depends on them and nowhere else."""
+    w, inp = inputs(T, n_shared=0)
+    few = Few(w, mxfp4=True, inp=inp)
+    few.call()
+    torch.cuda.synchronize()
+    want, idx = few.y[:T].clone(), few.idx[:T].clone()
+    # W2: column block 1 of row 33 of every expert; rows are 128 to a tile, K = f = 256
+    sf = few.mats["w2"][1].view(w.N * w.d // 128, w.f // 128, 512)
+    sf[0::w.d // 128, 0, 16 * (33 % 32) + 4 * (33 // 32) + 1] = 255
+    few.call()
+    torch.cuda.synchronize()
+    bad = torch.isnan(few.y[:T])
+    assert bad[:, 33].all() and bad.sum() == T
+    assert torch.equal(few.y[:T][~bad], want[~bad])
+    # W1: every scale of one expert; its tokens lose every output
+    few = Few(w, mxfp4=True, inp=inp)
+    e = int(idx[0, 0])
+    few.mats["w1"][1].view(w.N, -1)[e] = 255
+    few.call()
+    torch.cuda.synchronize()
+    hit = (idx == e).any(1)
+    assert hit.any() and torch.isnan(few.y[:T][hit]).all() and torch.equal(few.y[:T][~hit], want[~hit])
