@@ -471,6 +471,11 @@ struct Product<Mxfp4, DOWN, NT> {
 #pragma unroll
     for (int n = 0; n < NT; ++n) ts[n] = 8 * n + (lane >> 2) < t.n ? token_scale<DOWN>(t, tb, 8 * n + (lane >> 2)) : 0.f;
   }
+  // the sums of columns 2 tq and 2 tq + 1 without their rows' scales
+  __device__ __forceinline__ void unscale(float s0, float s1) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[i >> 2][0][i & 3] *= i & 1 ? s1 : s0;
+  }
   // columns by token: row i (or -1) of column g
   __device__ __forceinline__ void scale_of(const Tile& t, const Tables& tb, int i) {
     ts[0] = i >= 0 ? token_scale<DOWN>(t, tb, i) : 0.f;
@@ -760,15 +765,16 @@ __device__ __forceinline__ void run_down_by_token(const Args& a, Tables& tb, Wal
   while (w.next(t)) {
     // this lane's tokens: column g of the operand, columns 2 tq and 2 tq + 1 of the result
     uint32_t cols = 0;
-    float w0 = 0.f, w1 = 0.f;
+    float w0 = 0.f, w1 = 0.f, s0 = 1.f, s1 = 1.f;
     int mine = -1;
     for (int i = 0; i < t.n; ++i) {
       const int tok = t.sh ? i : tb.row_tok[t.row + i];
-      float v = t.sh ? tb.shw[tok] : tb.row_w[t.row + i];
-      if (C::MX) v *= inverse_pow2(token_scale<true>(t, tb, i));
+      const float v = t.sh ? tb.shw[tok] : tb.row_w[t.row + i];
+      // a product of the two could fall below fp32's normal numbers
+      const float s = C::MX ? inverse_pow2(token_scale<true>(t, tb, i)) : 1.f;
       cols |= 1u << tok;
-      if (tok == 2 * (lane & 3)) w0 = v;
-      if (tok == 2 * (lane & 3) + 1) w1 = v;
+      if (tok == 2 * (lane & 3)) { w0 = v; s0 = s; }
+      if (tok == 2 * (lane & 3) + 1) { w1 = v; s1 = s; }
       if (tok == (lane >> 2)) mine = i;
     }
     p.init(t, tb, lane, cols);
@@ -780,6 +786,7 @@ __device__ __forceinline__ void run_down_by_token(const Args& a, Tables& tb, Wal
       if (lane == 0) mbar_arrive(&tb.empty[r.stage]);
       r.next(C::STAGES);
     }
+    if constexpr (C::MX) p.unscale(s0, s1);
     p.fold(w0, w1, (cols >> (2 * (lane & 3))) & 1u, (cols >> (2 * (lane & 3) + 1)) & 1u, lane);
     if (!t.last) continue;
     const int wk = p.QT == 4 ? warp : warp >> 2;

@@ -141,3 +141,18 @@ def test_a_nan_scale_over_nonzero_codes_is_nan(T):
     torch.cuda.synchronize()
     hit = (idx == e).any(1)
     assert hit.any() and torch.isnan(few.y[:T][hit]).all() and torch.equal(few.y[:T][~hit], want[~hit])
+
+
+@pytest.mark.parametrize("T", [2, 6, 12])
+def test_small_weights_of_small_hidden_rows(T):
+    """The same with blocks of 2^108: no sum leaves fp32 on the way, and neither the weight nor
+    the hidden row's scale may lose bits to the other."""
+    w, inp = inputs(T, score="softmax", renorm=False, n_shared=0)
+    for n, e in (("w3", -117), ("w2", 108)):
+        scale(inp[n], e)
+    inp["w2"][0] = 0
+    inp["logit_offset"] = torch.zeros(w.N, device="cuda")
+    inp["logit_offset"][0] = 14.0
+    few = Few(w, mxfp4=True, inp=inp)
+    few.call()
+    few.check(routing=False)
