@@ -167,8 +167,11 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 def _stream(stream=None) -> Optional[int]:
     if stream is None:
-        # the handle alone: a Stream object around it costs 3 us of a call's 11
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        # the handle alone, where torch has it: a Stream object around it costs 3 us of a call's 11
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:
+            return raw(torch.cuda.current_device())
+        stream = torch.cuda.current_stream()
     return stream.cuda_stream
 
 

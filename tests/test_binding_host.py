@@ -116,3 +116,17 @@ def test_grouped_ffn_takes_rows_of_the_8_bit_type(reach):
         a[n] = a[n].view(torch.float8_e4m3fn)
     with pytest.raises(Reached):
         reach(cfg, a)
+
+
+# ------------------------------------------------------------------ the stream's handle
+def test_the_current_streams_handle_without_the_private_name(monkeypatch):
+    """Every entry point takes the current stream's handle from a private function of torch; a
+    torch without it still has the stream object's."""
+    class Stream:
+        cuda_stream = 77
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: Stream)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 55, raising=False)
+    assert L._stream() == 55 and L._stream(Stream) == 77
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
+    assert L._stream() == 77
