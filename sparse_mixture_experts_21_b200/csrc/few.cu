@@ -453,12 +453,15 @@ struct Product<float, DOWN, NT> {
 
 // MXFP4: a warp takes all four 16-row tiles on its share of the columns, so that a token's
 // conversion to fp16 serves them all.  Codes go to fp16 exactly; a block's two MMAs make a
-// sum of 32 columns, which the row's block scale multiplies in fp32.  Bound by its own
-// instructions, not by HBM: about 35 for the 512 codes of a 16-row tile's block, 16 of them
-// the conversion of 4-bit codes, where HBM would allow 47 at one a clock.  The block-scaled
-// tensor cores take the codes as they are, but not at this shape: an M = 128 x K = 32 MMA
-// costs ~200 cycles however few tokens there are, 800 for the 8.7 KB of codes that HBM
-// brings in 357 (measured with that kernel: 1.93 ms for 24 tokens against this one's 1.02).
+// sum of 32 columns, which the row's block scale multiplies in fp32.  About 35 instructions for
+// the 512 codes of a 16-row tile's block, 16 of them the conversion of 4-bit codes; at HBM's rate
+// a block arrives every 47 issue slots of an SM.  They would fit, but the warps issue in only 52%
+// of the slots (24 tokens, 64 experts of 2048, d = 7168) with no pipe full: they wait for shared
+// memory and for one another at the tiles' ends.  Without the products the call with 256 experts
+// takes 575 us, with them 0.97 ms.  The block-scaled tensor cores take the codes as they are, but
+// with the weights as the 128-row operand an M = 128 x K = 32 MMA costs ~200 cycles however few
+// tokens there are, 800 for the 8.7 KB of codes that HBM brings in 357 (1.93 ms for 24 tokens);
+// the weights as the 256-column operand are untried.
 template <bool DOWN, int NT>
 struct Product<Mxfp4, DOWN, NT> {
   using C = Cfg<Mxfp4>;

@@ -39,7 +39,9 @@ __device__ __forceinline__ uint32_t f32_e2m1(const float* f) {
   return r;
 }
 
-// Eight E2M1 codes of a word to four pairs of fp16 (exact), in order.
+// Eight E2M1 codes of a word to four pairs of fp16 (exact), in order.  Read all four: with
+// nvcc 12.9.86, where nothing reads the results of the upper bytes, those of the lower ones came
+// out as zeros (tried: whole, masked and 2-byte words; a shifted word with all four read is right).
 __device__ __forceinline__ void e2m1_f16(uint32_t w, uint32_t* o) {
   asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
       "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
@@ -149,8 +151,7 @@ quant_kernel(const XT* __restrict__ x, int64_t n16, int cols, uint2* __restrict_
 
 // Memory-bound.  A thread owns 8 consecutive elements (4 fp32), so a warp's stores are
 // contiguous: 32768 x 7168 in 111 us to bf16, 197 us to fp32 (5.4 TB/s; 264 us with 8 fp32 a
-// thread).  It converts its whole word either way: the conversion of a shifted or 2-byte word
-// whose upper bytes nothing reads came out as zeros.
+// thread).  It reads all of a word's results either way, as e2m1_f16 wants.
 template <typename YT>
 __global__ void __launch_bounds__(256)
 dequant_kernel(const uint32_t* __restrict__ q, const uint8_t* __restrict__ sf, int64_t n, int cols,
