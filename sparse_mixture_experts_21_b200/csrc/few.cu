@@ -455,7 +455,7 @@ struct Product<float, DOWN, NT> {
 // conversion to fp16 serves them all.  Codes go to fp16 exactly; a block's two MMAs make a
 // sum of 32 columns, which the row's block scale multiplies in fp32.  About 35 instructions for
 // the 512 codes of a 16-row tile's block, 16 of them the conversion of 4-bit codes; at HBM's rate
-// a block arrives every 47 issue slots of an SM.  They would fit, but the warps issue in only 52%
+// a block arrives every 47 issue slots of an SM.  They would fit, but the warps issue in only 51%
 // of the slots (24 tokens, 64 experts of 2048, d = 7168) with no pipe full: they wait for shared
 // memory and for one another at the tiles' ends.  Without the products the call with 256 experts
 // takes 575 us, with them 0.97 ms.  The block-scaled tensor cores take the codes as they are, but
