@@ -57,3 +57,27 @@ def test_an_output_dropped_while_the_current_stream_reads_it():
     lay.forward_few(other, s)
     torch.cuda.synchronize()
     assert torch.equal(kept, want)
+
+
+def test_a_side_stream_inside_a_capture():
+    """A step that forks to a side stream and drops y within the capture, replayed on new inputs."""
+    w = small("mxfp4")
+    inp = make_inputs(w, "cuda")
+    lay = MoELayer(w, inp, "cuda", update_bias=False)
+    x, out = inp["x"].clone(), torch.empty_like(inp["x"])
+    lay.forward_few(x)
+    torch.cuda.synchronize()
+    main, side, g = torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=main):
+        for _ in range(2):
+            side.wait_stream(main)
+            y = lay.forward_few(x, side)
+            main.wait_stream(side)
+            out.copy_(y)
+            del y
+    for scale in (1.0, 0.5, 2.0):
+        x.copy_(inp["x"] * scale)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, lay.forward_few(x))
+    assert L.moe_device_status() == L.MOE_OK
