@@ -458,7 +458,7 @@ struct Product<float, DOWN, NT> {
 // a block arrives every 47 issue slots of an SM.  They would fit, but the warps issue in only 51%
 // of the slots (24 tokens, 64 experts of 2048, d = 7168) with no pipe full: they wait for shared
 // memory and for one another at the tiles' ends.  Without the products the call with 256 experts
-// takes 575 us, with them 0.97 ms.  The block-scaled tensor cores take the codes as they are, but
+// takes 575 us, with them 1 ms.  The block-scaled tensor cores take the codes as they are, but
 // with the weights as the 128-row operand an M = 128 x K = 32 MMA costs ~200 cycles however few
 // tokens there are, 800 for the 8.7 KB of codes that HBM brings in 357 (1.93 ms for 24 tokens);
 // the weights as the 256-column operand are untried.
